@@ -87,6 +87,11 @@ typedef enum {
 #define RLK_DEVERR_TARGET 0x1u
 #define RLK_DEVERR_TIMEOUT 0x2u
 #define RLK_DEVERR_SCALE 0x4u   /* a transition std s_b was not a positive finite number */
+#define RLK_DEVERR_PROBS 0x8u   /* a row gives no distribution: see rlk_token_probs, rlk_draft_verify */
+
+/* Element types of the entry points that take more than one. */
+#define RLK_TYPE_BF16 0
+#define RLK_TYPE_F32 1
 
 /* Bytes of workspace that rlk_linear_logp_fwd (for_backward == 0) or both
  * rlk_linear_logp_fwd and rlk_linear_logp_bwd (for_backward != 0) need for
@@ -271,6 +276,60 @@ rlk_status rlk_transition_logp(const float* x, const float* v, const float* prev
                                const float* a, const float* c, const float* s, int64_t B,
                                int64_t n, float* mean_out, float* logp, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/* Probabilities of rows of logits, and verification of drafted tokens: the
+ * rollout side of the head (the logits of rlk_gemm_bf16_f32, or a serving
+ * engine's).  Both take rows with a stride, in elements, and both need a
+ * workspace of rlk_sampling_workspace_bytes() bytes, 256-byte aligned, whose
+ * first word is the device error word: zero it once; the library sets bits and
+ * never clears them.  It holds nothing else, so calls may share it and overlap.
+ * Types are RLK_TYPE_BF16 or RLK_TYPE_F32.  Every row's (sequence's) result is
+ * independent, bit for bit, of how many there are and of its position.
+ *
+ * rlk_token_probs: p[r][v] = exp(x[r][v] / tau - lse of the row), V entries of
+ * each of R rows (row strides ld_logits, ld_probs >= V), with tau =
+ * row_temperature[r] (device, [R] fp32) or, where that is NULL, `temperature`.
+ * tau = 0 is greedy: one at the maximum (the least index of several), zero
+ * elsewhere.  Logits of -inf get zero.  Computed in fp32 and rounded once to
+ * the type of probs.  A row of which nothing is left (all -inf) is written as
+ * zeros; one with a NaN, with +inf at tau > 0, or with a row temperature that
+ * is negative, not finite or so small that log2(e) / tau is not, as NaN; both
+ * set RLK_DEVERR_PROBS.  probs may be the logits' own memory where type and
+ * stride are equal.
+ * Sizes: 1 <= V < 2^31, R < 2^28, strides < 2^31.  R = 0 is a no-op.  One
+ * launch.
+ *
+ * rlk_draft_verify: B sequences with up to K drafted tokens each (draft_lens
+ * [B] int64, clamped to [0, K], or NULL: all K).  With p_i, the target's
+ * probabilities at draft position i (target_probs [B][K+1][V], strides
+ * target_stride_b, target_stride_k, the V entries contiguous) and q_i the
+ * draft's (draft_probs [B][K][V], or NULL: the draft had no distribution and
+ * counts as certain of its tokens), draft i with token d is accepted while
+ *     u_accept[b][i] q_i(d) < p_i(d).
+ * At the first draft n that is not, the next token is drawn from
+ * r(v) = max(0, p_n(v) - q_n(v)); after the last one from r = p_n.  It is the
+ * least v with r(0) + ... + r(v) > u_sample[b] (r(0) + ... + r(V-1)); for
+ * u_sample >= 1 (or NaN) the last v with r(v) > 0.  Where the residual is zero
+ * everywhere, r = p_n.  Products, differences and sums are fp64.
+ * Writes tokens [B][K+1] int64 (the accepted drafts, the drawn token, then -1)
+ * and num_accepted [B] int64.  A draft outside [0, V) within its sequence's
+ * length is not accepted and sets RLK_DEVERR_TARGET; where r has no positive
+ * entry, or its sum is not finite, the drawn token is -1 and RLK_DEVERR_PROBS
+ * is set.  Strides may be 0 (shared rows).  K = 0 draws one token per sequence
+ * (draft_tokens, u_accept, draft_probs are not read).
+ * Sizes: 1 <= V < 2^31, K < 2^20, B < 2^28.  B = 0 is a no-op.  One launch. */
+size_t rlk_sampling_workspace_bytes(void);
+rlk_status rlk_token_probs(const void* logits, int logits_type, int64_t R, int64_t V,
+                           int64_t ld_logits, float temperature, const float* row_temperature,
+                           void* probs, int probs_type, int64_t ld_probs, void* workspace,
+                           size_t workspace_bytes, void* stream);
+rlk_status rlk_draft_verify(const void* target_probs, int64_t target_stride_b,
+                            int64_t target_stride_k, const void* draft_probs,
+                            int64_t draft_stride_b, int64_t draft_stride_k, int probs_type,
+                            const int64_t* draft_tokens, const float* u_accept,
+                            const float* u_sample, const int64_t* draft_lens, int64_t B,
+                            int64_t K, int64_t V, int64_t* tokens, int64_t* num_accepted,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* Batch-invariant deterministic dense GEMM on the same tensor-core mainloop as
  * every kernel above (also its self-check): C[M,N] fp32 = sum_k A[m,k] B[n,k]

@@ -6,6 +6,7 @@ is not a B200 the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -18,6 +19,7 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "rlk.h")
 
 RLK_DEVERR_TARGET = 0x1
 RLK_DEVERR_TIMEOUT = 0x2
+RLK_DEVERR_PROBS = 0x8
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -566,3 +568,149 @@ def rlk_transition_logp(x, v, prev, a, c, s, want_mean=False, out=None, workspac
                                      _ptr(workspace), workspace.numel(), _stream(stream)),
            "rlk_transition_logp")
     return mean, logp
+
+
+_TYPE_IDS = {torch.bfloat16: 0, torch.float32: 1}  # RLK_TYPE_*
+
+
+def _scope(dev, stream):
+    """The context a call on tensors of `dev` runs in: that device is current,
+    and what the call allocates belongs to the stream it enqueues on."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+        return torch.cuda.stream(stream)
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _on(dev, t, dtypes, name, shape):
+    if t.device != dev or t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" %
+                         (name, " or ".join(str(d) for d in dtypes), list(shape), dev))
+
+
+def _scratch(workspace, dev):
+    if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
+    return workspace
+
+
+_samp_fns = None
+
+
+def _samp():
+    global _samp_fns
+    if _samp_fns is None:
+        L = lib()
+        L.rlk_sampling_workspace_bytes.argtypes = []
+        L.rlk_sampling_workspace_bytes.restype = ctypes.c_size_t
+        L.rlk_token_probs.argtypes = [_P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_float, _P, _P,
+                                      ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]
+        L.rlk_token_probs.restype = ctypes.c_int
+        L.rlk_draft_verify.argtypes = [_P, _I64, _I64, _P, _I64, _I64, ctypes.c_int, _P, _P, _P, _P,
+                                       _I64, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P]
+        L.rlk_draft_verify.restype = ctypes.c_int
+        _samp_fns = L
+    return _samp_fns
+
+
+def sampling_workspace(device=None):
+    """The zeroed workspace (an error word) of rlk_token_probs and
+    rlk_draft_verify; calls may share it."""
+    return torch.zeros(int(_samp().rlk_sampling_workspace_bytes()), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def _row_stride(t, name):
+    """The stride of `t` viewed as rows of its last dimension."""
+    if not t.is_cuda or t.dtype not in _TYPE_IDS or t.dim() < 1:
+        raise ValueError("%s must be a CUDA bf16 or fp32 tensor" % name)
+    if t.is_contiguous():
+        return t.shape[-1]
+    lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    ld = lead[-1][1] if lead else t.shape[-1]
+    if (t.shape[-1] != 1 and t.stride(-1) != 1) or ld < t.shape[-1] or \
+            any(a[1] != b[0] * b[1] for a, b in zip(lead, lead[1:])):
+        raise ValueError("%s must be rows of contiguous entries, one stride apart" % name)
+    return ld
+
+
+def rlk_token_probs(logits, temperature=1.0, dtype=None, out=None, workspace=None, stream=None):
+    """softmax(logits / temperature) over the last dimension, in `dtype` (bf16 or
+    fp32; the logits' own by default).  logits [..., V] bf16 or fp32, rows one
+    stride apart; temperature a number or a CUDA fp32 tensor of the leading
+    shape; 0 is greedy.  `out` may be the logits themselves."""
+    dev = logits.device
+    ld = _row_stride(logits, "logits")
+    V = logits.shape[-1]
+    if V < 1:
+        raise ValueError("logits must have at least one entry per row")
+    R = logits.numel() // V
+    row_t = None
+    if isinstance(temperature, torch.Tensor):
+        row_t, temperature = temperature, 1.0
+        _on(dev, row_t, (torch.float32,), "temperature", tuple(logits.shape[:-1]))
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty(logits.shape, dtype=dtype or logits.dtype, device=dev)
+            if out.dtype not in _TYPE_IDS:
+                raise ValueError("dtype must be bf16 or fp32")
+        elif out.device != dev or out.shape != logits.shape or (dtype and out.dtype != dtype):
+            raise ValueError("out must have the logits' shape and device, and the given dtype")
+        ld_out = _row_stride(out, "out")
+        workspace = sampling_workspace(dev) if workspace is None else _scratch(workspace, dev)
+        _check(_samp().rlk_token_probs(logits.data_ptr(), _TYPE_IDS[logits.dtype], R, V, ld,
+                                       float(temperature), _ptr(row_t), out.data_ptr(),
+                                       _TYPE_IDS[out.dtype], ld_out, workspace.data_ptr(),
+                                       workspace.numel(), _stream(stream)),
+               "rlk_token_probs")
+    return out
+
+
+def rlk_draft_verify(target_probs, draft_probs, draft_tokens, u_accept, u_sample, draft_lens=None,
+                     out=None, workspace=None, stream=None):
+    """(tokens [B, K+1] int64, num_accepted [B] int64) of B sequences of up to K
+    drafted tokens: target_probs [B, K+1, V] and draft_probs [B, K, V] (or None:
+    drafts without a distribution), both bf16 or both fp32 with contiguous rows;
+    draft_tokens [B, K] int64; u_accept [B, K] and u_sample [B] fp32 uniform
+    numbers in [0, 1); draft_lens [B] int64.  tokens holds the accepted drafts,
+    the token drawn after them, then -1."""
+    dev = target_probs.device
+    if target_probs.dim() != 3 or not target_probs.is_cuda or target_probs.dtype not in _TYPE_IDS:
+        raise ValueError("target_probs must be a CUDA bf16 or fp32 tensor [B, K+1, V]")
+    B, K, V = target_probs.shape
+    K -= 1
+    if K < 0 or V < 1:
+        raise ValueError("target_probs must be [B, K+1, V] with V >= 1")
+    if V > 1 and target_probs.stride(2) != 1:
+        raise ValueError("target_probs must have contiguous rows")
+    q_sb = q_sk = 0
+    if draft_probs is not None:
+        if draft_probs.device != dev or draft_probs.dtype != target_probs.dtype or \
+                tuple(draft_probs.shape) != (B, K, V) or (V > 1 and draft_probs.stride(2) != 1):
+            raise ValueError("draft_probs must be [B, K, V] of target_probs' type and device, "
+                             "with contiguous rows")
+        q_sb, q_sk = draft_probs.stride(0), draft_probs.stride(1)
+    _on(dev, draft_tokens, (torch.int64,), "draft_tokens", (B, K))
+    _on(dev, u_accept, (torch.float32,), "u_accept", (B, K))
+    _on(dev, u_sample, (torch.float32,), "u_sample", (B,))
+    if draft_lens is not None:
+        _on(dev, draft_lens, (torch.int64,), "draft_lens", (B,))
+    with _scope(dev, stream):
+        if out is None:
+            out = (torch.empty(B, K + 1, dtype=torch.int64, device=dev),
+                   torch.empty(B, dtype=torch.int64, device=dev))
+        else:
+            _on(dev, out[0], (torch.int64,), "tokens", (B, K + 1))
+            _on(dev, out[1], (torch.int64,), "num_accepted", (B,))
+        workspace = sampling_workspace(dev) if workspace is None else _scratch(workspace, dev)
+        _check(_samp().rlk_draft_verify(target_probs.data_ptr(), target_probs.stride(0),
+                                        target_probs.stride(1), _ptr(draft_probs), q_sb, q_sk,
+                                        _TYPE_IDS[target_probs.dtype], draft_tokens.data_ptr(),
+                                        u_accept.data_ptr(), u_sample.data_ptr(), _ptr(draft_lens),
+                                        B, K, V, out[0].data_ptr(), out[1].data_ptr(),
+                                        workspace.data_ptr(), workspace.numel(), _stream(stream)),
+               "rlk_draft_verify")
+    return out
