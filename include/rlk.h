@@ -277,6 +277,55 @@ rlk_status rlk_transition_logp(const float* x, const float* v, const float* prev
                                int64_t n, float* mean_out, float* logp, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* Distillation of the head from a teacher's top logits (what a draft model, or
+ * a smaller student, is trained on): with z, lse and p of the student as at the
+ * top of this file, and for each row K slots of a teacher's vocab ids and
+ * logits g,
+ *
+ *   a_k   = g_k / teacher_temperature
+ *   q_k   = exp(a_k - L),  L = log sum_k exp(a_k), or teacher_lse[t] where given
+ *   loss  = sum_k q_k (log q_k - z[id_k] + lse)
+ *   dx[v] = dloss (Q p[v] - sum_k q_k 1[v = id_k]) / temperature,  Q = sum_k q_k
+ *
+ * and dHidden, dW from dx as for rlk_linear_logp_bwd.  Without teacher_lse the
+ * teacher's distribution is renormalised over its slots (Q = 1); with it
+ * (the teacher's own log-sum-exp, or zeros for log-probabilities) the weights
+ * are the teacher's probabilities and the rest of its mass carries no loss.
+ *  - teacher_ids [T][K] int64: a vocab id, or -1 for a slot that is not used
+ *    (its logit is not looked at).  Ids may come in any order; an id given twice
+ *    counts twice.  teacher_logits [T][K] of logits_type; -inf weighs nothing.
+ *    A row without a used slot, or with all of them at -inf, has loss 0 and no
+ *    gradient.  Any other id outside [0, V) sets RLK_DEVERR_TARGET (forward) and
+ *    makes the row's loss NaN; both passes leave the slot out.
+ *  - teacher_lse [T] fp32 or NULL.  1 <= K <= 256 (more:
+ *    RLK_ERR_UNSUPPORTED_SHAPE); teacher_temperature > 0 and finite.
+ *  - fwd writes loss [T] and lse [T] fp32; lse equals rlk_linear_logp_fwd's bit
+ *    for bit.  A row's loss does not depend on the other rows, on T or on the
+ *    order of its (distinct) ids.
+ *  - bwd takes the forward's lse and dloss [T] fp32; overwrites dHidden [T,H]
+ *    bf16 and dW [V,H], of dW_type (fp32, or bf16 rounded once from the fp32
+ *    sum), 16-byte aligned; dW NULL leaves it out (a frozen head) and saves its
+ *    product.  As in rlk_linear_logp_bwd, dx is rounded to bf16 before the two
+ *    products.  T = 0 zeroes dW.
+ *  - Workspace: rlk_linear_distill_workspace_bytes (0 for unsupported sizes), its
+ *    first 256 bytes zeroed once; one buffer serves both passes, which keep
+ *    nothing in it between them. */
+size_t rlk_linear_distill_workspace_bytes(int64_t T, int64_t H, int64_t V, int64_t K,
+                                          int for_backward);
+rlk_status rlk_linear_distill_fwd(const rlk_bf16* hidden, const rlk_bf16* W,
+                                  const int64_t* teacher_ids, const void* teacher_logits,
+                                  int logits_type, const float* teacher_lse, int64_t T, int64_t H,
+                                  int64_t V, int64_t K, float temperature,
+                                  float teacher_temperature, float* loss, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
+                                  const int64_t* teacher_ids, const void* teacher_logits,
+                                  int logits_type, const float* teacher_lse, int64_t T, int64_t H,
+                                  int64_t V, int64_t K, float temperature,
+                                  float teacher_temperature, const float* lse, const float* dloss,
+                                  rlk_bf16* dHidden, void* dW, int dW_type, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Probabilities of rows of logits, and verification of drafted tokens: the
  * rollout side of the head (the logits of rlk_gemm_bf16_f32, or a serving
  * engine's).  Both take rows with a stride, in elements, and both need a

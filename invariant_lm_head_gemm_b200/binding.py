@@ -714,3 +714,142 @@ def rlk_draft_verify(target_probs, draft_probs, draft_tokens, u_accept, u_sample
                                         workspace.data_ptr(), workspace.numel(), _stream(stream)),
                "rlk_draft_verify")
     return out
+
+
+_dis_fns = None
+
+
+def _dis():
+    global _dis_fns
+    if _dis_fns is None:
+        L = lib()
+        L.rlk_linear_distill_workspace_bytes.argtypes = [_I64, _I64, _I64, _I64, ctypes.c_int]
+        L.rlk_linear_distill_workspace_bytes.restype = ctypes.c_size_t
+        L.rlk_linear_distill_fwd.argtypes = [_P, _P, _P, _P, ctypes.c_int, _P, _I64, _I64, _I64, _I64,
+                                             ctypes.c_float, ctypes.c_float, _P, _P, _P,
+                                             ctypes.c_size_t, _P]
+        L.rlk_linear_distill_fwd.restype = ctypes.c_int
+        L.rlk_linear_distill_bwd.argtypes = [_P, _P, _P, _P, ctypes.c_int, _P, _I64, _I64, _I64, _I64,
+                                             ctypes.c_float, ctypes.c_float, _P, _P, _P, _P,
+                                             ctypes.c_int, _P, ctypes.c_size_t, _P]
+        L.rlk_linear_distill_bwd.restype = ctypes.c_int
+        _dis_fns = L
+    return _dis_fns
+
+
+def make_distill_workspace(T: int, H: int, V: int, K: int, for_backward: bool = True, device=None):
+    """A workspace tensor (uint8) for the distillation of T rows with K slots,
+    its error word zeroed."""
+    n = int(_dis().rlk_linear_distill_workspace_bytes(T, H, V, K, 1 if for_backward else 0))
+    if n == 0:
+        raise ValueError("unsupported sizes T=%d H=%d V=%d K=%d" % (T, H, V, K))
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:256].zero_()
+    return ws
+
+
+def _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse):
+    _req(hidden, torch.bfloat16, "hidden", 2)
+    dev = hidden.device
+    T, H = hidden.shape
+    if W.dim() != 2 or teacher_ids.dim() != 2:
+        raise ValueError("W must be [V, H] and teacher_ids [T, K]")
+    V, K = W.shape[0], teacher_ids.shape[1]
+    _on(dev, W, (torch.bfloat16,), "W", (V, H))
+    _on(dev, teacher_ids, (torch.int64,), "teacher_ids", (T, K))
+    _on(dev, teacher_logits, tuple(_TYPE_IDS), "teacher_logits", (T, K))
+    if teacher_lse is not None:
+        _on(dev, teacher_lse, (torch.float32,), "teacher_lse", (T,))
+    return dev, T, H, V, K
+
+
+def rlk_linear_distill_fwd(hidden, W, teacher_ids, teacher_logits, temperature=1.0,
+                           teacher_temperature=None, teacher_lse=None, workspace=None, out=None,
+                           stream=None):
+    """(loss, lse) [T] fp32 of distilling hidden [T,H] bf16 through the head W
+    [V,H] bf16 from a teacher's top logits: teacher_ids [T,K] int64 (-1: unused
+    slot), teacher_logits [T,K] fp32 or bf16, divided by teacher_temperature (the
+    student's by default); teacher_lse [T] fp32 gives the teacher's own
+    log-sum-exp instead of renormalising over the slots."""
+    dev, T, H, V, K = _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse)
+    if teacher_temperature is None:
+        teacher_temperature = temperature
+    with _scope(dev, stream):
+        if workspace is None:
+            workspace = make_distill_workspace(T, H, V, K, False, dev)
+        _scratch(workspace, dev)
+        if out is None:
+            out = tuple(torch.empty(T, dtype=torch.float32, device=dev) for _ in range(2))
+        loss, lse = out
+        _on(dev, loss, (torch.float32,), "loss", (T,))
+        _on(dev, lse, (torch.float32,), "lse", (T,))
+        _check(_dis().rlk_linear_distill_fwd(
+            _ptr(hidden), _ptr(W), _ptr(teacher_ids), _ptr(teacher_logits),
+            _TYPE_IDS[teacher_logits.dtype], _ptr(teacher_lse), T, H, V, K, float(temperature),
+            float(teacher_temperature), _ptr(loss), _ptr(lse), _ptr(workspace), workspace.numel(),
+            _stream(stream)), "rlk_linear_distill_fwd")
+    return loss, lse
+
+
+def rlk_linear_distill_bwd(hidden, W, teacher_ids, teacher_logits, temperature, lse, dloss,
+                           teacher_temperature=None, teacher_lse=None, workspace=None, out=None,
+                           dW_dtype=torch.float32, stream=None):
+    """(dHidden [T,H] bf16, dW [V,H]) for the loss gradients dloss [T] fp32 and the
+    forward's lse; dW in dW_dtype (fp32 or bf16), or None for a frozen head."""
+    dev, T, H, V, K = _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse)
+    _on(dev, lse, (torch.float32,), "lse", (T,))
+    _on(dev, dloss, (torch.float32,), "dloss", (T,))
+    if dW_dtype is not None and dW_dtype not in _TYPE_IDS:
+        raise ValueError("dW_dtype must be fp32, bf16 or None")
+    if teacher_temperature is None:
+        teacher_temperature = temperature
+    with _scope(dev, stream):
+        if workspace is None:
+            workspace = make_distill_workspace(T, H, V, K, True, dev)
+        _scratch(workspace, dev)
+        if out is None:
+            out = (torch.empty(T, H, dtype=torch.bfloat16, device=dev),
+                   None if dW_dtype is None else torch.empty(V, H, dtype=dW_dtype, device=dev))
+        dHidden, dW = out
+        _on(dev, dHidden, (torch.bfloat16,), "dHidden", (T, H))
+        if (dW is None) != (dW_dtype is None):
+            raise ValueError("out must hold dW where dW_dtype is given, and only there")
+        if dW is not None:
+            _on(dev, dW, (dW_dtype,), "dW", (V, H))
+        _check(_dis().rlk_linear_distill_bwd(
+            _ptr(hidden), _ptr(W), _ptr(teacher_ids), _ptr(teacher_logits),
+            _TYPE_IDS[teacher_logits.dtype], _ptr(teacher_lse), T, H, V, K, float(temperature),
+            float(teacher_temperature), _ptr(lse), _ptr(dloss), _ptr(dHidden), _ptr(dW),
+            _TYPE_IDS[dW_dtype or torch.float32], _ptr(workspace), workspace.numel(),
+            _stream(stream)), "rlk_linear_distill_bwd")
+    return dHidden, dW
+
+
+class LinearDistill(torch.autograd.Function):
+    """autograd wrapper: loss [T] = LinearDistill.apply(hidden, W, teacher_ids,
+    teacher_logits, temperature, teacher_temperature=None, teacher_lse=None).
+    Gradients flow to hidden and W (bf16); a W that needs none costs none."""
+
+    @staticmethod
+    def forward(ctx, hidden, W, teacher_ids, teacher_logits, temperature=1.0,
+                teacher_temperature=None, teacher_lse=None):
+        T, H = hidden.shape
+        ws = make_distill_workspace(T, H, W.shape[0], teacher_ids.shape[1],
+                                    any(ctx.needs_input_grad[:2]), hidden.device)
+        loss, lse = rlk_linear_distill_fwd(hidden, W, teacher_ids, teacher_logits, temperature,
+                                           teacher_temperature, teacher_lse, ws)
+        ctx.save_for_backward(hidden, W, teacher_ids, teacher_logits, teacher_lse, lse)
+        ctx.temperatures = (temperature, teacher_temperature)
+        ctx.ws = ws
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        hidden, W, teacher_ids, teacher_logits, teacher_lse, lse = ctx.saved_tensors
+        temperature, teacher_temperature = ctx.temperatures
+        dH, dW = rlk_linear_distill_bwd(hidden, W, teacher_ids, teacher_logits, temperature, lse,
+                                        dloss.float().contiguous(), teacher_temperature,
+                                        teacher_lse, ctx.ws,
+                                        dW_dtype=W.dtype if ctx.needs_input_grad[1] else None)
+        return dH if ctx.needs_input_grad[0] else None, dW, None, None, None, None, None

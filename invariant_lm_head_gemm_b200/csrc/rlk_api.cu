@@ -222,7 +222,7 @@ rlk_status write_chunk_words(uint32_t* words, int64_t n, uint32_t seq, cudaStrea
   return RLK_OK;
 }
 
-std::atomic<int> g_max_clusters[3][kMaxDevices];
+std::atomic<int> g_max_clusters[kModes][kMaxDevices];
 
 // Launches pair_kernel<Mode> on clusters of two CTAs: at most one cluster per
 // unit and no more clusters than can be resident at once.  `cooperative`
@@ -282,7 +282,7 @@ rlk_status launch_pair(const typename ModeArgs<Mode>::type& args, long long tota
 // target falls in these rows, the target's scaled logit to ytgt.
 static_assert(kDecSplit == kBN * kFwdGroup, "both forward kernels must use the same splits");
 
-std::atomic<int> g_dec_max_clusters[2][3][kDecMaxRows / 16][kMaxDevices];  // store, form, N/16-1
+std::atomic<int> g_dec_max_clusters[3][3][kDecMaxRows / 16][kMaxDevices];  // fold, store or distill; form; N/16-1
 
 // The MMA width of the short-batch kernel for T rows: 16, or T rounded up to 32.
 int dec_width(int64_t T) { return T <= 16 ? 16 : static_cast<int>(ceil_div(T, 32) * 32); }
@@ -292,9 +292,11 @@ int dec_width(int64_t T) { return T <= 16 ? 16 : static_cast<int>(ceil_div(T, 32
 // CTA-pair form from there (its hidden map's box must then hold N / 2 rows);
 // `store` selects the plain GEMM epilogue instead of the online fold, and
 // `half` (with `store`, N <= kDecHalfMaxN) the half-height single-CTA form,
-// whose W map's box holds 64 rows and whose units cover 256 W rows.
-rlk_status launch_short(DecArgs& a, bool store, cudaStream_t st, bool half = false) {
-  if (half && (!store || a.N > kDecHalfMaxN)) return RLK_ERR_INVALID_ARG;
+// whose W map's box holds 64 rows and whose units cover 256 W rows; `distill`
+// picks up the logits at a teacher's ids (a.ep.dis) instead of a target's.
+rlk_status launch_short(DecArgs& a, bool store, cudaStream_t st, bool half = false,
+                        bool distill = false) {
+  if ((half && (!store || a.N > kDecHalfMaxN)) || (distill && store)) return RLK_ERR_INVALID_ARG;
   const bool pair = !half && a.N >= kDecPairMinN;
   constexpr uint32_t kSmemLimit = 227u * 1024u;
   a.stages = dec_stages(a.N, pair, kSmemLimit, half);
@@ -302,6 +304,8 @@ rlk_status launch_short(DecArgs& a, bool store, cudaStream_t st, bool half = fal
   const uint32_t smem = dec_smem_bytes(a.N, a.stages, pair, half);
   void (*kern)(DecArgs) =
       half ? decode_fwd_kernel<false, true, true>
+           : distill ? (pair ? decode_fwd_kernel<true, false, false, true>
+                             : decode_fwd_kernel<false, false, false, true>)
            : store ? (pair ? decode_fwd_kernel<true, true> : decode_fwd_kernel<false, true>)
                    : (pair ? decode_fwd_kernel<true, false> : decode_fwd_kernel<false, false>);
   int dev = 0;
@@ -325,7 +329,7 @@ rlk_status launch_short(DecArgs& a, bool store, cudaStream_t st, bool half = fal
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  std::atomic<int>& cache = g_dec_max_clusters[store ? 1 : 0][half ? 2 : pair ? 1 : 0][a.N / 16 - 1][dev];
+  std::atomic<int>& cache = g_dec_max_clusters[distill ? 2 : store ? 1 : 0][half ? 2 : pair ? 1 : 0][a.N / 16 - 1][dev];
   int mc = cache.load(std::memory_order_relaxed);
   if (mc == 0) {
     cfg.gridDim = dim3(kDecCluster);
@@ -351,7 +355,7 @@ rlk_status enqueue_fwd_partials_short(const rlk_bf16* hidden, const rlk_bf16* W,
                                       int64_t v0, float temperature, float* part_m, float* part_s,
                                       float* part_b, int64_t ldp, float* ytgt, uint32_t* err,
                                       cudaStream_t st, uint64_t wait_limit_ns = kWaitLimitNs,
-                                      int stall = 0) {
+                                      int stall = 0, const DistillRows* dis = nullptr) {
   DecArgs a;
   a.wait_limit_ns = wait_limit_ns;
   a.stall = stall;
@@ -371,18 +375,20 @@ rlk_status enqueue_fwd_partials_short(const rlk_bf16* hidden, const rlk_bf16* W,
   a.ep.v0 = v0;
   a.ep.scale_log2 = kLog2e / temperature;
   a.err = err;
+  a.ep.dis = dis ? *dis : DistillRows{};
   a.KB = static_cast<int>(H / kBK);
   a.NG = static_cast<int>(fwd_groups(Vloc));
-  return launch_short(a, false, st);
+  return launch_short(a, false, st, false, dis != nullptr);
 }
 
 rlk_status enqueue_fwd_partials(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t* targets,
                                 int64_t T, int64_t H, int64_t Vloc, int64_t v0, float temperature,
                                 float* part_m, float* part_s, float* part_b, int64_t ldp,
-                                float* ytgt, uint32_t* err, cudaStream_t st) {
+                                float* ytgt, uint32_t* err, cudaStream_t st,
+                                const DistillRows* dis = nullptr) {
   if (T <= kDecMaxT)
     return enqueue_fwd_partials_short(hidden, W, targets, T, H, Vloc, v0, temperature, part_m,
-                                      part_s, part_b, ldp, ytgt, err, st);
+                                      part_s, part_b, ldp, ytgt, err, st, kWaitLimitNs, 0, dis);
   FwdArgs a;
   // 3-D maps (one copy per operand and stage) when the driver takes them
   a.k3 = map_kmajor3(&a.hid_k, hidden, H, T, H) && map_kmajor3(&a.w_k, W, H, Vloc, H) ? 1 : 0;
@@ -406,7 +412,9 @@ rlk_status enqueue_fwd_partials(const rlk_bf16* hidden, const rlk_bf16* W, const
   a.NG = static_cast<int>(fwd_groups(Vloc));
   a.KB = static_cast<int>(H / kBK);
   a.total = static_cast<long long>(a.MT) * a.NG;
-  return launch_pair<kModeFwd>(a, a.total, false, st);
+  a.ep.dis = dis ? *dis : DistillRows{};
+  return dis ? launch_pair<kModeFwdDistill>(a, a.total, false, st)
+             : launch_pair<kModeFwd>(a, a.total, false, st);
 }
 
 // Forward, second half: merge the splits (layout [nshards][T][Gs]) in global
@@ -440,7 +448,8 @@ rlk_status enqueue_fwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
 // Backward over W rows [v0, v0 + Vloc) of a Vfull-row head (the whole head:
 // v0 = 0, Vloc = Vfull), chunked as the full head is.  dh_parts null: dHidden
 // accumulated over the chunks and written as bf16; else each chunk's fp32
-// product goes to dh_parts (EpiDh::kPart layout).
+// product goes to dh_parts (EpiDh::kPart layout).  `dis`: the distillation's
+// dlogits, with its loss gradients, a bf16 dW or (dW null) none.
 rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t* targets,
                        int64_t T, int64_t H, int64_t Vloc, int64_t v0, int64_t Vfull,
                        float temperature, const float* lse, const float* entropy,
@@ -448,9 +457,11 @@ rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
                        float* dh_parts, int64_t part_rows, int64_t part_chunks, float* dW,
                        uint8_t* ws, const Layout& L, cudaStream_t st,
                        uint64_t wait_limit_ns = kWaitLimitNs, int stall_first_h = 0,
-                       uint32_t* chunk_done = nullptr, uint32_t seq = 0) {
+                       uint32_t* chunk_done = nullptr, uint32_t seq = 0,
+                       const DistillRows* dis = nullptr, const float* dloss = nullptr,
+                       bool dw_bf16 = false) {
   BwdParams P;
-  P.plan = make_bwd_plan(T, H, Vloc, vchunk(Vfull));
+  P.plan = make_bwd_plan(T, H, Vloc, vchunk(Vfull), dW != nullptr);
   const BwdPlan& pl = P.plan;
   void* dx[kDxBuffers];
   for (int i = 0; i < kDxBuffers; ++i) {
@@ -505,12 +516,16 @@ rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
   P.stall_first_h = stall_first_h;
   P.chunk_done = chunk_done;
   P.seq = seq;
+  P.dis = dis ? *dis : DistillRows{};
+  P.dloss = dloss;
+  P.dw_bf16 = dw_bf16 ? 1 : 0;
 
   if (cudaMemsetAsync(cnt, 0, bwd_counter_words(pl) * 4, st) != cudaSuccess) return RLK_ERR_CUDA;
   // Units wait on units claimed earlier, and only running CTA pairs claim
   // units, so no pair ever waits on one that has not started: the launch needs
   // no co-residency guarantee.
-  return launch_pair<kModeBwd>(P, pl.total, false, st);
+  return dis ? launch_pair<kModeBwdDistill>(P, pl.total, false, st)
+             : launch_pair<kModeBwd>(P, pl.total, false, st);
 }
 
 }  // namespace
@@ -1181,6 +1196,168 @@ rlk_status rlk_linear_logp_fwd_noalloc(const rlk_bf16* hidden, const rlk_bf16* W
   if (cudaGetLastError() != cudaSuccess) return RLK_ERR_CUDA;
   g_calls[0].fetch_add(1);
   return RLK_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Distillation from a teacher's top logits (rlk_distill.cuh).
+// ---------------------------------------------------------------------------
+namespace rlk {
+namespace {
+
+// The sorted slots and their table behind a pass's own scratch, from `base`.
+struct DistillLayout {
+  size_t ids, logq, y, sum, count, first, end;
+  int64_t G;
+};
+
+DistillLayout distill_layout(size_t base, int64_t T, int64_t V, int64_t K, int shift) {
+  DistillLayout L;
+  const size_t t = static_cast<size_t>(T), k = static_cast<size_t>(K);
+  L.G = ceil_div(V, int64_t{1} << shift);
+  L.ids = base;
+  L.logq = L.ids + align256(t * k * 4);
+  L.y = L.logq + align256(t * k * 4);
+  L.sum = L.y + align256(t * k * 4);
+  L.count = L.sum + align256(t * 4);
+  L.first = L.count + align256(t * 4);
+  L.end = L.first + align256(t * static_cast<size_t>(L.G + 1) * 2);
+  return L;
+}
+
+DistillRows distill_rows(uint8_t* ws, const DistillLayout& L, int64_t K) {
+  DistillRows D;
+  D.ids = reinterpret_cast<int*>(ws + L.ids);
+  D.logq = reinterpret_cast<float*>(ws + L.logq);
+  D.y = reinterpret_cast<float*>(ws + L.y);
+  D.sum = reinterpret_cast<float*>(ws + L.sum);
+  D.count = reinterpret_cast<int*>(ws + L.count);
+  D.first = reinterpret_cast<uint16_t*>(ws + L.first);
+  D.ld = static_cast<int>(K);
+  D.entries = static_cast<int>(L.G + 1);
+  return D;
+}
+
+rlk_status check_distill(int64_t T, int64_t H, int64_t V, int64_t K, float temperature,
+                         float teacher_temperature, int logits_type) {
+  rlk_status s = check_sizes(T, H, V, temperature);
+  if (s != RLK_OK) return s;
+  if (K < 1 || !std::isfinite(teacher_temperature) || !(teacher_temperature > 0.f))
+    return RLK_ERR_INVALID_ARG;
+  if (logits_type != RLK_TYPE_BF16 && logits_type != RLK_TYPE_F32) return RLK_ERR_INVALID_ARG;
+  return K > kDisMaxK ? RLK_ERR_UNSUPPORTED_SHAPE : RLK_OK;
+}
+
+rlk_status enqueue_distill_prep(const int64_t* ids, const void* logits, int logits_type,
+                                const float* teacher_lse, int64_t T, int64_t V, int64_t K,
+                                float teacher_temperature, int64_t G, int shift,
+                                const DistillRows& D, cudaStream_t st) {
+  const unsigned blocks = static_cast<unsigned>(ceil_div(T, 4));
+  const int t = static_cast<int>(T), k = static_cast<int>(K), v = static_cast<int>(V),
+            g = static_cast<int>(G);
+  if (logits_type == RLK_TYPE_F32) {
+    distill_prep_kernel<float><<<blocks, 128, 0, st>>>(ids, static_cast<const float*>(logits),
+                                                       teacher_lse, t, k, v, g, shift,
+                                                       teacher_temperature, D);
+  } else {
+    distill_prep_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(
+        ids, static_cast<const __nv_bfloat16*>(logits), teacher_lse, t, k, v, g, shift,
+        teacher_temperature, D);
+  }
+  return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace rlk
+
+extern "C" {
+
+size_t rlk_linear_distill_workspace_bytes(int64_t T, int64_t H, int64_t V, int64_t K,
+                                          int for_backward) {
+  if (check_distill(T, H, V, K, 1.f, 1.f, RLK_TYPE_F32) != RLK_OK) return 0;
+  const Layout L = layout(T, H, V);
+  const size_t fwd = distill_layout(L.fwd_end, T, V, K, kDisFwdShift).end;
+  const size_t bwd = distill_layout(L.bwd_end, T, V, K, kDisBwdShift).end;
+  return for_backward ? std::max(fwd, bwd) : fwd;
+}
+
+rlk_status rlk_linear_distill_fwd(const rlk_bf16* hidden, const rlk_bf16* W,
+                                  const int64_t* teacher_ids, const void* teacher_logits,
+                                  int logits_type, const float* teacher_lse, int64_t T, int64_t H,
+                                  int64_t V, int64_t K, float temperature,
+                                  float teacher_temperature, float* loss, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  rlk_status s = check_distill(T, H, V, K, temperature, teacher_temperature, logits_type);
+  if (s != RLK_OK) return s;
+  if (T == 0) return RLK_OK;
+  if (!hidden || !W || !teacher_ids || !teacher_logits || !loss || !lse || !workspace)
+    return RLK_ERR_INVALID_ARG;
+  if (!aligned(hidden, 16) || !aligned(W, 16) || !aligned(workspace, 256) ||
+      !aligned(teacher_ids, 8) || !aligned(teacher_logits, logits_type == RLK_TYPE_F32 ? 4 : 2) ||
+      !aligned(teacher_lse, 4) || !aligned(loss, 4) || !aligned(lse, 4))
+    return RLK_ERR_MISALIGNED;
+  const Layout L = layout(T, H, V);
+  const DistillLayout DL = distill_layout(L.fwd_end, T, V, K, kDisFwdShift);
+  if (workspace_bytes < DL.end) return RLK_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  if ((s = check_device(&sms)) != RLK_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint32_t* err = reinterpret_cast<uint32_t*>(ws);
+  float* pm = reinterpret_cast<float*>(ws + L.pm);
+  float* ps = reinterpret_cast<float*>(ws + L.ps);
+  float* pb = reinterpret_cast<float*>(ws + L.pb);
+  const DistillRows D = distill_rows(ws, DL, K);
+  if ((s = enqueue_distill_prep(teacher_ids, teacher_logits, logits_type, teacher_lse, T, V, K,
+                                teacher_temperature, DL.G, kDisFwdShift, D, st)) != RLK_OK)
+    return s;
+  if ((s = enqueue_fwd_partials(hidden, W, nullptr, T, H, V, 0, temperature, pm, ps, pb,
+                                fwd_groups(V), reinterpret_cast<float*>(ws + L.yt), err, st,
+                                &D)) != RLK_OK)
+    return s;
+  distill_combine_kernel<<<static_cast<unsigned>(ceil_div(T, 8)), 256, 0, st>>>(
+      pm, ps, pb, D, static_cast<int>(T), static_cast<int>(fwd_groups(V)), loss, lse, err);
+  return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
+                                  const int64_t* teacher_ids, const void* teacher_logits,
+                                  int logits_type, const float* teacher_lse, int64_t T, int64_t H,
+                                  int64_t V, int64_t K, float temperature,
+                                  float teacher_temperature, const float* lse, const float* dloss,
+                                  rlk_bf16* dHidden, void* dW, int dW_type, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  rlk_status s = check_distill(T, H, V, K, temperature, teacher_temperature, logits_type);
+  if (s != RLK_OK) return s;
+  if (dW_type != RLK_TYPE_BF16 && dW_type != RLK_TYPE_F32) return RLK_ERR_INVALID_ARG;
+  if (!aligned(dW, 16)) return RLK_ERR_MISALIGNED;
+  int sms = 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if ((s = check_device(&sms)) != RLK_OK) return s;
+    const size_t bytes = static_cast<size_t>(V) * H * (dW_type == RLK_TYPE_F32 ? 4 : 2);
+    return !dW || cudaMemsetAsync(dW, 0, bytes, st) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+  }
+  if (!hidden || !W || !teacher_ids || !teacher_logits || !lse || !dloss || !dHidden || !workspace)
+    return RLK_ERR_INVALID_ARG;
+  if (!aligned(hidden, 16) || !aligned(W, 16) || !aligned(dHidden, 16) ||
+      !aligned(workspace, 256) || !aligned(teacher_ids, 8) ||
+      !aligned(teacher_logits, logits_type == RLK_TYPE_F32 ? 4 : 2) || !aligned(teacher_lse, 4) ||
+      !aligned(lse, 4) || !aligned(dloss, 4))
+    return RLK_ERR_MISALIGNED;
+  const Layout L = layout(T, H, V);
+  const DistillLayout DL = distill_layout(L.bwd_end, T, V, K, kDisBwdShift);
+  if (workspace_bytes < DL.end) return RLK_ERR_WORKSPACE_TOO_SMALL;
+  if ((s = check_device(&sms)) != RLK_OK) return s;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const DistillRows D = distill_rows(ws, DL, K);
+  if ((s = enqueue_distill_prep(teacher_ids, teacher_logits, logits_type, teacher_lse, T, V, K,
+                                teacher_temperature, DL.G, kDisBwdShift, D, st)) != RLK_OK)
+    return s;
+  return enqueue_bwd(hidden, W, nullptr, T, H, V, 0, V, temperature, lse, nullptr, nullptr, nullptr,
+                     dHidden, nullptr, 0, 0, static_cast<float*>(dW), ws, L, st, kWaitLimitNs, 0,
+                     nullptr, 0, &D, dloss, dW_type == RLK_TYPE_BF16);
 }
 
 }  // extern "C"

@@ -48,7 +48,7 @@ struct BwdMaps {
 struct BwdPlan {
   int T, H, V, ldx, NC, MT, NH;
   int RT_full, RT_last;  // 256-column recompute tiles per chunk
-  int VT_full, VT_last;  // 256-row dW tiles per chunk (equal to RT_*)
+  int VT_full, VT_last;  // 256-row dW tiles per chunk (equal to RT_*, or 0 without dW)
   int valid_last;        // vocab entries of the last chunk
   int KB_R;              // k-blocks of a recompute tile (H / 64)
   int KB_D;              // k-blocks of a dW tile (ceil(T / 64))
@@ -85,6 +85,10 @@ struct BwdParams {
   uint32_t* chunk_done;  // null, or [NC] words: chunk c's word is set to `seq` once its
                          // dHidden and dW units are done (for an exchange that overlaps)
   uint32_t seq;
+  // distillation (kModeBwdDistill): instead of targets, entropy, dlogp, dentropy
+  DistillRows dis;
+  const float* dloss;
+  int dw_bf16;        // dW points to bf16
 };
 
 enum : int { kUnitR = 0, kUnitH = 1, kUnitD = 2 };
@@ -114,7 +118,9 @@ __host__ __device__ inline int bwd_group_size(const BwdPlan& P, int g) {
 // (a multiple of 256).
 __host__ inline long long bwd_total_units(const BwdPlan& P);
 
-__host__ inline BwdPlan make_bwd_plan(int64_t T, int64_t H, int64_t V, int64_t ldx) {
+// Without dW (`with_dw` false) there are no D units.
+__host__ inline BwdPlan make_bwd_plan(int64_t T, int64_t H, int64_t V, int64_t ldx,
+                                      bool with_dw = true) {
   BwdPlan p;
   p.T = static_cast<int>(T);
   p.H = static_cast<int>(H);
@@ -124,10 +130,10 @@ __host__ inline BwdPlan make_bwd_plan(int64_t T, int64_t H, int64_t V, int64_t l
   p.MT = static_cast<int>((T + kPairM - 1) / kPairM);
   p.NH = static_cast<int>((H + kBN - 1) / kBN);
   p.RT_full = p.ldx / kBN;
-  p.VT_full = p.ldx / kPairM;
+  p.VT_full = with_dw ? p.ldx / kPairM : 0;
   p.valid_last = static_cast<int>(V - static_cast<int64_t>(p.NC - 1) * p.ldx);
   p.RT_last = (p.valid_last + kBN - 1) / kBN;
-  p.VT_last = (p.valid_last + kPairM - 1) / kPairM;
+  p.VT_last = with_dw ? (p.valid_last + kPairM - 1) / kPairM : 0;
   p.KB_R = static_cast<int>(H / kBK);
   p.KB_D = static_cast<int>((T + kBK - 1) / kBK);
   p.total = bwd_total_units(p);

@@ -139,9 +139,10 @@ __host__ __device__ constexpr int dec_stages(int N, bool pair, uint32_t limit, b
   return S >= 2 ? S : 0;
 }
 
-template <bool kPair, bool kStore = false, bool kHalf = false>
+template <bool kPair, bool kStore = false, bool kHalf = false, bool kDistill = false>
 __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid_constant__ DecArgs P) {
   static_assert(!kHalf || (kStore && !kPair), "the half-height form is a single-CTA store form");
+  static_assert(!kDistill || !kStore, "distillation folds its logits");
   constexpr int MR = DecForm<kPair>::kMaxRows;  // batch rows a hand buffer holds
   constexpr int RB = kHalf ? kDecHalfRows : kBM;                  // W rows per CTA tile
   constexpr uint32_t kABox = static_cast<uint32_t>(RB) * kBK * 2u;  // one RB x 64 W box
@@ -457,7 +458,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
           // row-major per batch row (Y[row][W row of the tile]), in the memory of
           // the four transposition tiles.
           const int t = lane;
-          const int64_t tgt = t < P.ep.T ? P.ep.targets[t] - P.ep.v0 : -1;
+          int64_t tgt = -1;
+          int f0 = 0, f1 = 0;  // distillation: the row's slots in this split
+          if constexpr (kDistill) {
+            if (t < P.ep.T) dis_range(P.ep.dis, t, static_cast<int>(u), f0, f1);
+          } else {
+            if (t < P.ep.T) tgt = P.ep.targets[t] - P.ep.v0;
+          }
           float* Y = XT;
           if (warp != 2 && k > 0 && !warp_wait(xfree_bar, (k - 1) & 1u)) break;
           if (rank > 0 && !warp_wait_cluster(hfull_bar(h, 0), hph)) break;
@@ -505,6 +512,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
               y[4 * i + 2] = fwd_scale(f.z, P.ep.scale_log2);
               y[4 * i + 3] = fwd_scale(f.w, P.ep.scale_log2);
             }
+            if constexpr (kDistill)
+              dis_capture(P.ep.dis, static_cast<size_t>(t) * P.ep.dis.ld, y, tile0 + c * 32, f0, f1);
             if (t < P.ep.T) fwd_chunk_update(y, tile0 + c * 32, P.ep.V, tgt, P.ep.ytgt + t, m, s, b);
           }
           mbar_arrive(xfree_bar);
@@ -525,7 +534,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
         }
         for (int blk = 0; blk < nblk; ++blk, ++g) {
           const int t = blk * 32 + lane;
-          const int64_t tgt = t < P.ep.T ? P.ep.targets[t] - P.ep.v0 : -1;  // issued early
+          int64_t tgt = -1;  // loaded early, as the range is
+          int f0 = 0, f1 = 0;
+          if constexpr (kDistill) {
+            if (t < P.ep.T) dis_range(P.ep.dis, t, static_cast<int>(u), f0, f1);
+          } else {
+            if (t < P.ep.T) tgt = P.ep.targets[t] - P.ep.v0;
+          }
           // 1. this block's 32 columns of the accumulator, transposed through the
           //    warp's tile: lane l ends with batch row blk*32+l over the chunk
           if (N == 16) {
@@ -555,6 +570,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] = fwd_scale(xt[i * kDecXStride + lane], P.ep.scale_log2);
           __syncwarp();  // the tile is free for the next block
+          if constexpr (kDistill) {  // before the wait below: not part of the chain
+            dis_capture(P.ep.dis, static_cast<size_t>(t) * P.ep.dis.ld, y, col0, f0, f1);
+            __syncwarp();
+          }
           // 2. the rows' running triples
           float m = kMaskLogit, s = 0.f, b = 0.f;
           if (q == 0) {

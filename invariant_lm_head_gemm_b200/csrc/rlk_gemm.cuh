@@ -31,6 +31,64 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// A teacher's top logits for the distillation kernels (rlk_distill.cuh): per row,
+// the used slots sorted by vocab id, and how many lie below each table column.
+struct DistillRows {
+  int* ids;          // [T][ld] sorted ids
+  float* logq;       // [T][ld] log weights
+  float* y;          // [T][ld] the student's scaled logits there (forward)
+  float* sum;        // [T] sum of the weights
+  int* count;        // [T] used slots, and a flag
+  uint16_t* first;   // [T][entries] slots with ids below (column << shift)
+  int ld;            // slots per row
+  int entries;       // table entries per row
+};
+
+constexpr int kDisMaxK = 256;
+constexpr int kDisEnd = 0x7fffffff;  // past every vocab id
+constexpr int kDisBad = 1 << 30;     // flag beside a row's count: an id outside [0, V)
+constexpr int kDisFwdShift = 9;      // columns per table entry: a forward split (512) ...
+constexpr int kDisBwdShift = 8;      // ... and a recompute tile (256)
+
+// The weight of a slot from its stored logarithm.
+__device__ __forceinline__ float dis_weight(float logq) { return expf(logq); }
+
+// Picks y[d] of a register array.
+__device__ __forceinline__ float dis_select(const float (&y)[32], int d) {
+  float v = y[0];
+#pragma unroll
+  for (int j = 1; j < 32; ++j) v = (j == d) ? y[j] : v;
+  return v;
+}
+
+// The logits y at this row's ids within columns col0 .. col0 + 31, for a walk in
+// ascending columns: `cur` is the next sorted slot, `nxt` its id.
+__device__ __forceinline__ void dis_capture_next(const DistillRows& D, size_t row0,
+                                                 const float (&y)[32], int col0, int& cur, int end,
+                                                 int& nxt) {
+  while (nxt < col0 + 32) {
+    D.y[row0 + cur] = dis_select(y, nxt - col0);
+    ++cur;
+    nxt = cur < end ? D.ids[row0 + cur] : kDisEnd;
+  }
+}
+
+// The slots of row `row` in table column g.
+__device__ __forceinline__ void dis_range(const DistillRows& D, int row, int g, int& f0, int& f1) {
+  const uint16_t* f = D.first + static_cast<size_t>(row) * D.entries + g;
+  f0 = f[0];
+  f1 = f[1];
+}
+
+// The same for a chunk met on its own, among the slots [f0, f1) of its split.
+__device__ __forceinline__ void dis_capture(const DistillRows& D, size_t row0,
+                                            const float (&y)[32], int col0, int f0, int f1) {
+  for (int i = f0; i < f1; ++i) {
+    const int d = D.ids[row0 + i] - col0;
+    if (d >= 0 && d < 32) D.y[row0 + i] = dis_select(y, d);
+  }
+}
+
 // =====================================================================
 // Epilogue policies.  Each provides Params, State and
 //   begin_unit(p, st, row, mt, g)   once per unit, row = global M index
@@ -99,23 +157,37 @@ struct EpiFwd {
     int ldp;           // row stride of part_*: at least this W's vocab splits
     int64_t v0;        // global vocab index of this W's first row (0 unless a shard)
     float scale_log2;  // log2(e) / tau
+    DistillRows dis;   // distillation: the ids to pick y up at, instead of a target
   };
   struct State {
     float m, s, b;
     int64_t tgt;
     int row;
     bool valid;
+    int cur, end, nxt;  // distillation: the slots of this split still to come
   };
 
-  __device__ static void begin_unit(const Params& p, State& st, int row, int, int) {
+  template <bool kDistill>
+  __device__ static void begin_unit(const Params& p, State& st, int row, int g) {
     st.row = row;
     st.valid = row < p.T;
-    st.tgt = st.valid ? p.targets[row] - p.v0 : -1;  // local column of the target
+    if constexpr (kDistill) {
+      st.tgt = -1;
+      st.cur = st.end = 0;
+      st.nxt = kDisEnd;
+      if (st.valid) {
+        dis_range(p.dis, row, g, st.cur, st.end);
+        if (st.cur < st.end) st.nxt = p.dis.ids[static_cast<size_t>(row) * p.dis.ld + st.cur];
+      }
+    } else {
+      st.tgt = st.valid ? p.targets[row] - p.v0 : -1;  // local column of the target
+    }
     st.m = kMaskLogit;
     st.s = 0.f;
     st.b = 0.f;
   }
 
+  template <bool kDistill>
   __device__ static void tile(const Params& p, State& st, uint32_t taddr, int nt) {
 #pragma unroll 1
     for (int c = 0; c < kBN / 32; ++c) {
@@ -124,6 +196,11 @@ struct EpiFwd {
       float y[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) y[j] = fwd_scale(__uint_as_float(r[j]), p.scale_log2);
+      if constexpr (kDistill) {
+        dis_capture_next(p.dis, static_cast<size_t>(st.row) * p.dis.ld, y, nt * kBN + c * 32, st.cur,
+                         st.end, st.nxt);
+        __syncwarp();
+      }
       fwd_chunk_update(y, nt * kBN + c * 32, p.V, st.tgt, p.ytgt + st.row, st.m, st.s, st.b);
     }
   }
@@ -137,6 +214,28 @@ struct EpiFwd {
     }
   }
 };
+
+// Writes one warp's 32 x 32 chunk of dlogits, lane = row, as bf16 to
+// dX[warp_row0 .. +32, loc0 .. +32] through the 2 KB shared-memory buffer `buf`
+// (layout and store as EpiDlogits::tile describes).
+__device__ __forceinline__ void store_dx_chunk(const float (&dx)[32], const CUtensorMap* store_map,
+                                               uint32_t buf, int lane, int loc0, int warp_row0) {
+  if (lane == 0) bulk_wait_read_le1();  // the store two chunks back has read `buf`
+  __syncwarp();
+  const uint32_t row_addr = buf + lane * 64u;
+  const uint32_t sw = static_cast<uint32_t>(lane >> 1) & 3u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    st_shared_v4(row_addr + ((static_cast<uint32_t>(q) ^ sw) << 4), pack_bf16x2(dx[8 * q + 0], dx[8 * q + 1]),
+                 pack_bf16x2(dx[8 * q + 2], dx[8 * q + 3]), pack_bf16x2(dx[8 * q + 4], dx[8 * q + 5]),
+                 pack_bf16x2(dx[8 * q + 6], dx[8 * q + 7]));
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(store_map, buf, loc0, warp_row0);
+    bulk_commit_group();
+  }
+}
 
 // Backward recompute: the same logits tile, turned into bf16 dlogits
 //   dx = (dlogp (1[v = target] - p) - dentropy p (z - E_p z)) / tau
@@ -226,25 +325,7 @@ struct EpiDlogits {
 #pragma unroll
         for (int j = 0; j < 32; ++j) dx[j] = (j == d) ? dx[j] + st.hot : dx[j];
       }
-      if (any_row) {
-        const uint32_t buf = stage + (c & 1) * 2048u;
-        if (lane == 0) bulk_wait_read_le1();  // the store two chunks back has read `buf`
-        __syncwarp();
-        const uint32_t row_addr = buf + lane * 64u;
-        const uint32_t sw = static_cast<uint32_t>(lane >> 1) & 3u;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          st_shared_v4(row_addr + ((static_cast<uint32_t>(q) ^ sw) << 4), pack_bf16x2(dx[8 * q + 0], dx[8 * q + 1]),
-                       pack_bf16x2(dx[8 * q + 2], dx[8 * q + 3]),
-                       pack_bf16x2(dx[8 * q + 4], dx[8 * q + 5]),
-                       pack_bf16x2(dx[8 * q + 6], dx[8 * q + 7]));
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(store_map, buf, loc0, warp_row0);
-          bulk_commit_group();
-        }
-      }
+      if (any_row) store_dx_chunk(dx, store_map, stage + (c & 1) * 2048u, lane, loc0, warp_row0);
     }
   }
 
@@ -374,6 +455,33 @@ struct EpiStore {
   __device__ static void end_unit(const Params&, State&, int) {}
 };
 
+// The same tile stored as bf16 (one rounding of the fp32 sum), where dW goes
+// straight into a bf16 gradient: half the bytes written, and no pass to convert.
+struct EpiStoreBf16 {
+  __device__ static void tile(__nv_bfloat16* out, int rows, int ncols, int ld, int row,
+                              uint32_t taddr, int nt) {
+#pragma unroll 1
+    for (int c = 0; c < kBN / 32; ++c) {
+      const int col0 = nt * kBN + c * 32;
+      if (col0 >= ncols) break;  // warp-uniform
+      uint32_t r[32];
+      tmem_ld32(taddr + c * 32, r);
+      if (row >= rows) continue;
+      // ncols = H is a multiple of 64: a chunk is whole
+      uint4* dst = reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * ld + col0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint4 w;
+        w.x = pack_bf16x2(__uint_as_float(r[8 * q + 0]), __uint_as_float(r[8 * q + 1]));
+        w.y = pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]));
+        w.z = pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]));
+        w.w = pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7]));
+        dst[q] = w;
+      }
+    }
+  }
+};
+
 // Fixed-order merge of the forward's per-split triples into
 // lse = ln2 (M + log2 S), entropy = ln2 (log2 S - B / S),
 // logp = ln2 (y_target - M - log2 S).
@@ -393,6 +501,18 @@ __device__ __forceinline__ Triple merge_triple(Triple x, Triple y) {
   r.s = ax * x.s + ay * y.s;
   r.b = ax * fmaf(x.m - mn, x.s, x.b) + ay * fmaf(y.m - mn, y.s, y.b);
   return r;
+}
+
+__device__ __forceinline__ Triple merge_lanes(Triple acc) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    Triple o;
+    o.m = __shfl_xor_sync(0xffffffffu, acc.m, off);
+    o.s = __shfl_xor_sync(0xffffffffu, acc.s, off);
+    o.b = __shfl_xor_sync(0xffffffffu, acc.b, off);
+    acc = merge_triple(acc, o);
+  }
+  return acc;
 }
 
 // Partials are laid out [shard][T][Gs]: split g of row t sits in shard g / Gs
@@ -415,14 +535,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     const size_t i = (static_cast<size_t>(g / Gs) * T + t) * Gs + g % Gs;
     acc = merge_triple(acc, Triple{pm[i], ps[i], pb[i]});
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    Triple o;
-    o.m = __shfl_xor_sync(0xffffffffu, acc.m, off);
-    o.s = __shfl_xor_sync(0xffffffffu, acc.s, off);
-    o.b = __shfl_xor_sync(0xffffffffu, acc.b, off);
-    acc = merge_triple(acc, o);
-  }
+  acc = merge_lanes(acc);
   if (lane != 0) return;
   const float l2s = log2f(acc.s);
   lse[t] = kLn2 * (acc.m + l2s);

@@ -27,6 +27,7 @@
 #pragma once
 
 #include "rlk_bwd.cuh"
+#include "rlk_distill.cuh"
 #include "rlk_gemm.cuh"
 
 namespace rlk {
@@ -38,7 +39,10 @@ constexpr uint32_t kPAStage = kSubK * kSubA;  // a stage's A: 32 KB
 constexpr uint32_t kPBStage = kSubK * kSubB;  // a stage's B: 32 KB
 constexpr int kRing = 4;                      // units in flight through the pair's broadcast ring
 
-enum : int { kModeFwd = 0, kModeBwd = 1, kModeGemm = 2 };
+enum : int { kModeFwd = 0, kModeBwd = 1, kModeGemm = 2, kModeFwdDistill = 3, kModeBwdDistill = 4 };
+constexpr int kModes = 5;
+constexpr bool is_fwd(int mode) { return mode == kModeFwd || mode == kModeFwdDistill; }
+constexpr bool is_bwd(int mode) { return mode == kModeBwd || mode == kModeBwdDistill; }
 
 // Shared memory per mode: three operand stages (192 KB); the backward's
 // dlogit epilogue adds 16 KB of TMA store staging (two 2 KB buffers per
@@ -46,7 +50,7 @@ enum : int { kModeFwd = 0, kModeBwd = 1, kModeGemm = 2 };
 template <int Mode>
 struct PipeCfg {
   static constexpr int kStages = 3;
-  static constexpr uint32_t kStaging = Mode == kModeBwd ? 4 * 4096 : 0;
+  static constexpr uint32_t kStaging = is_bwd(Mode) ? 4 * 4096 : 0;
   static constexpr int kNumBars = 2 * kStages + 5 + 2 * kRing;
   static constexpr size_t kSmemBytes =
       1024 + kStages * (kPAStage + kPBStage) + kStaging + kNumBars * 8 + 64;
@@ -93,6 +97,14 @@ struct ModeArgs<kModeBwd> {
 template <>
 struct ModeArgs<kModeGemm> {
   using type = GemmArgs;
+};
+template <>
+struct ModeArgs<kModeFwdDistill> {
+  using type = FwdArgs;
+};
+template <>
+struct ModeArgs<kModeBwdDistill> {
+  using type = BwdParams;
 };
 
 // What one unit loads and computes.
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // leader's producer claims the next unit from a global counter, in
   // ascending order, and broadcasts it through a kRing-slot ring to the
   // leader's MMA issuer, the peer's producer and both CTAs' epilogues.
-  constexpr bool kDynamic = Mode == kModeBwd;
+  constexpr bool kDynamic = is_bwd(Mode);
   auto static_unit = [&](uint32_t k) -> long long {
     const long long u = pair + static_cast<long long>(k) * npairs;
     return u < total ? u : -1;
@@ -394,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < 0) break;
         const Job j = make_job(P, u);
         if (j.type < 0) break;
-        if constexpr (Mode == kModeBwd) {
+        if constexpr (is_bwd(Mode)) {
           const BwdPlan& pl = P.plan;
           if (j.type == kUnitH) {
             // the test hook asks one unit too many of the first dHidden unit
@@ -555,13 +567,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Job j = make_job(P, u);
       if (j.type < 0) break;
       typename EpiFwd::State fst;
-      if constexpr (Mode == kModeFwd) EpiFwd::begin_unit(P.ep, fst, j.mt * kPairM + row_off, 0, 0);
+      constexpr bool kDistill = Mode == kModeFwdDistill || Mode == kModeBwdDistill;
+      if constexpr (is_fwd(Mode))
+        EpiFwd::begin_unit<kDistill>(P.ep, fst, j.mt * kPairM + row_off, j.nt / P.group);
       for (int t = 0; t < j.ntiles; ++t, ++tc) {
         const int acc = tc & 1;
         const uint32_t use = tc >> 1;
         if (ep_leader) {
           bool ok = mbar_wait_bounded(tfull_bar(acc), use & 1u, abort_flag, err, lim);
-          if constexpr (Mode == kModeBwd) {
+          if constexpr (is_bwd(Mode)) {
             const BwdPlan& pl = P.plan;
             if (ok && j.type == kUnitR && j.c >= kDxBuffers) {
               const int c3 = j.c - kDxBuffers;
@@ -585,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN;
         const int row = j.mt * kPairM + row_off;
-        if constexpr (Mode == kModeFwd) {
-          EpiFwd::tile(P.ep, fst, taddr, j.nt + t);
+        if constexpr (is_fwd(Mode)) {
+          EpiFwd::tile<kDistill>(P.ep, fst, taddr, j.nt + t);
         } else if constexpr (Mode == kModeGemm) {
           EpiStore::State st;
           EpiStore::begin_unit(P.ep, st, row, 0, 0);
@@ -594,24 +608,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const BwdPlan& pl = P.plan;
           if (j.type == kUnitR) {
-            EpiDlogits::Params p;
-            p.targets = P.targets;
-            p.lse = P.lse;
-            p.entropy = P.entropy;
-            p.dlogp = P.dlogp;
-            p.dentropy = P.dentropy;
-            p.err = err;
-            p.T = pl.T;
-            p.V = pl.V;
-            p.c0 = j.c * pl.ldx;
-            p.v0 = P.v0;
-            p.Vfull = P.Vfull;
-            p.scale_log2 = P.scale_log2;
-            p.inv_tau = P.inv_tau;
-            EpiDlogits::State st;
-            EpiDlogits::begin_unit(p, st, row, 0, 0);
-            EpiDlogits::tile(p, st, taddr, j.nt, &P.maps.dx_st[j.c % kDxBuffers],
-                             sStage + q * 4096u, lane, row - lane);
+            if constexpr (kDistill) {
+              EpiDistill::Params p;
+              p.D = P.dis;
+              p.lse = P.lse;
+              p.dloss = P.dloss;
+              p.T = pl.T;
+              p.V = pl.V;
+              p.c0 = j.c * pl.ldx;
+              p.scale_log2 = P.scale_log2;
+              p.inv_tau = P.inv_tau;
+              EpiDistill::State st;
+              EpiDistill::begin_unit(p, st, row);
+              EpiDistill::tile(p, st, taddr, j.nt, &P.maps.dx_st[j.c % kDxBuffers],
+                               sStage + q * 4096u, lane, row - lane);
+            } else {
+              EpiDlogits::Params p;
+              p.targets = P.targets;
+              p.lse = P.lse;
+              p.entropy = P.entropy;
+              p.dlogp = P.dlogp;
+              p.dentropy = P.dentropy;
+              p.err = err;
+              p.T = pl.T;
+              p.V = pl.V;
+              p.c0 = j.c * pl.ldx;
+              p.v0 = P.v0;
+              p.Vfull = P.Vfull;
+              p.scale_log2 = P.scale_log2;
+              p.inv_tau = P.inv_tau;
+              EpiDlogits::State st;
+              EpiDlogits::begin_unit(p, st, row, 0, 0);
+              EpiDlogits::tile(p, st, taddr, j.nt, &P.maps.dx_st[j.c % kDxBuffers],
+                               sStage + q * 4096u, lane, row - lane);
+            }
           } else if (j.type == kUnitH) {
             EpiDh::Params p;
             p.acc = P.dh_acc;
@@ -630,6 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             EpiDh::State st;
             EpiDh::begin_unit(p, st, row, 0, 0);
             EpiDh::tile(p, st, taddr, j.nt);
+          } else if (kDistill && P.dw_bf16 != 0) {
+            EpiStoreBf16::tile(reinterpret_cast<__nv_bfloat16*>(P.dW) +
+                                   static_cast<size_t>(j.c) * pl.ldx * pl.H,
+                               bwd_chunk_valid(pl, j.c), pl.H, pl.H, row, taddr, j.nt);
           } else {
             EpiStore::Params p;
             p.out = P.dW + static_cast<size_t>(j.c) * pl.ldx * pl.H;
@@ -650,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
           }
         }
-        if constexpr (Mode == kModeBwd) {
+        if constexpr (is_bwd(Mode)) {
           if (j.type == kUnitR && lane == 0) bulk_wait_all();  // dX tiles written
           epilogue_bar();  // every store of this CTA's half of the unit is done or issued
           if (ep_leader) {
@@ -676,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if constexpr (Mode == kModeFwd) {
+      if constexpr (is_fwd(Mode)) {
         if (go) EpiFwd::end_unit(P.ep, fst, j.nt / P.group);
       }
     }
@@ -684,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (Mode == kModeBwd) {
+  if constexpr (is_bwd(Mode)) {
     // After a timed-out wait some chunks never complete: publish every chunk
     // word anyway, so that a stream waiting on them is released (the error
     // word already says the results are not to be used).
