@@ -10,7 +10,7 @@
 // row alignment (an odd V puts every row at another offset) and keeps the
 // element-to-thread map, and with it the order of the sums, the same for all
 // rows.
-#include <cfloat>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -68,146 +68,135 @@ struct ProbArgs {
   void* p;
   const float* row_tau;
   int64_t ldx, ldp;
-  int64_t V;
+  int V;
+  int slice;  // entries per CTA of the cluster
   float tau;
   unsigned* err;
 };
 
-template <typename TIn, typename TOut, int kThreads, int kN, bool kResident>
-__global__ void __launch_bounds__(kThreads) probs_kernel(const ProbArgs P) {
+template <typename TIn, typename TOut, int kThreads, int kN, int kBlocks, bool kResident>
+__global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const ProbArgs P) {
   constexpr int kWarps = kThreads / 32;
+  constexpr int kStep = kN * kThreads;
   __shared__ uint2 pairs[kProbMaxCluster * kProbMaxWarps];
   uint32_t C, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   cluster_started();
-  const int64_t row = blockIdx.x / C;
+  const int row = blockIdx.x / C;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const TIn* x = static_cast<const TIn*>(P.x) + row * P.ldx;
-  TOut* p = static_cast<TOut*>(P.p) + row * P.ldp;
-  const int64_t step = static_cast<int64_t>(C) * kThreads;
-  const int64_t i0 = static_cast<int64_t>(rank) * kThreads + threadIdx.x;
+  const int lo = static_cast<int>(min(static_cast<int64_t>(rank) * P.slice, static_cast<int64_t>(P.V)));
+  const int n = min(P.slice, P.V - lo);  // this CTA's entries
+  const int t = threadIdx.x;
+  const TIn* x = static_cast<const TIn*>(P.x) + row * P.ldx + lo;
+  TOut* p = static_cast<TOut*>(P.p) + row * P.ldp + lo;
 
   float v[kN];
+  auto load = [&](int b) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = t < n - b - j * kThreads ? to_f32(x[b + t + j * kThreads]) : -INFINITY;
+  };
   float m = -INFINITY;
-  bool nan = false;
   const float tau = P.row_tau ? P.row_tau[row] : P.tau;
   const float k = kSampLog2e / tau;
   const bool greedy = tau == 0.f;
-  if constexpr (kResident) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int64_t i = i0 + j * step;
-      v[j] = i < P.V ? to_f32(x[i]) : -INFINITY;
-    }
+  for (int b = 0; b < (kResident ? 1 : n); b += kStep) {
+    load(b);
 #pragma unroll
     for (int j = 0; j < kN; ++j) m = fmaxf(m, v[j]);
-  } else {
-    for (int64_t b = i0; b < P.V; b += kN * step) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) v[j] = b + j * step < P.V ? to_f32(x[b + j * step]) : -INFINITY;
-#pragma unroll
-      for (int j = 0; j < kN; ++j) m = fmaxf(m, v[j]);
-    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
   const float mref = m == -INFINITY ? 0.f : m;  // -inf - -inf would be NaN
 
-  // this warp's sum relative to its maximum; its first maximum for tau = 0
-  float s = 0.f;
-  int64_t first = INT64_MAX;
-  auto take = [&](float xv, int64_t i) {
-    if (!greedy) {
-      const float e = ex2_approx((xv - mref) * k);
-      s += e;
-      return e;
+  if (greedy) {
+    // this warp's first maximum; a NaN travels as the maximum
+    int first = INT_MAX;
+    bool nan = false;
+    for (int b = 0; b < (kResident ? 1 : n); b += kStep) {
+      if (!kResident) load(b);
+#pragma unroll
+      for (int j = kN - 1; j >= 0; --j) {
+        const int i = b + t + j * kThreads;
+        nan |= v[j] != v[j];
+        if (i < n && v[j] == m) first = min(first, lo + i);
+      }
     }
-    nan |= i < P.V && xv != xv;
-    if (i < P.V && xv == m && i < first) first = i;
-    return 0.f;
-  };
-  if constexpr (kResident) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] = take(v[j], i0 + j * step);
-  } else {
-    for (int64_t b = i0; b < P.V; b += kN * step) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) v[j] = b + j * step < P.V ? to_f32(x[b + j * step]) : -INFINITY;
-#pragma unroll
-      for (int j = 0; j < kN; ++j) take(v[j], b + j * step);
-    }
-  }
-  uint2 mine;
-  if (!greedy) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    mine = make_uint2(__float_as_uint(m), __float_as_uint(s));
-  } else {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(kFull, first, o));
-    // V < 2^31: an index fits; a NaN in the row travels as the maximum
     if (__any_sync(kFull, nan)) m = NAN;
-    mine = make_uint2(__float_as_uint(m),
-                      static_cast<uint32_t>(min(first, static_cast<int64_t>(0x7fffffff))));
-  }
-  cluster_all_started();
-  if (lane < C)
-    st_cluster_v2(mapa_shared(smem_u32(&pairs[rank * kWarps + warp]), lane), mine.x, mine.y);
-  cluster_sync();
-
-  const int n = static_cast<int>(C) * kWarps;
-  float gm = -INFINITY, S = 0.f, bad = 0.f;
-  for (int i = lane; i < n; i += 32) {
-    const float mi = __uint_as_float(pairs[i].x);
-    gm = fmaxf(gm, mi);
-    bad += mi != mi ? 1.f : 0.f;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, o));
-  if (!greedy) {
-    const float gref = gm == -INFINITY ? 0.f : gm;
-    for (int i = lane; i < n; i += 32)
-      S += __uint_as_float(pairs[i].y) * ex2_approx((__uint_as_float(pairs[i].x) - gref) * k);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(kFull, S, o);
-    // nothing left by the mask: all zeros; a NaN or +inf logit, or a
-    // temperature that is not a positive number: all NaN
-    const bool usable = tau > 0.f && k > 0.f && k < INFINITY && S == S;
-    const bool empty = usable && gm == -INFINITY;
-    float f = ex2_approx((mref - gref) * k) / S;
-    if (m == -INFINITY || empty) f = 0.f;
-    if (!usable) f = NAN;
-    if constexpr (kResident) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const int64_t i = i0 + j * step;
-        if (i < P.V) store_as(p + i, v[j] * f);
-      }
-    } else {
-      for (int64_t b = i0; b < P.V; b += kN * step) {
-#pragma unroll
-        for (int j = 0; j < kN; ++j) v[j] = b + j * step < P.V ? to_f32(x[b + j * step]) : 0.f;
-#pragma unroll
-        for (int j = 0; j < kN; ++j)
-          if (b + j * step < P.V) store_as(p + b + j * step, ex2_approx((v[j] - mref) * k) * f);
-      }
+    cluster_all_started();
+    if (lane < C)
+      st_cluster_v2(mapa_shared(smem_u32(&pairs[rank * kWarps + warp]), lane), __float_as_uint(m),
+                    static_cast<uint32_t>(first));
+    cluster_sync();
+    float gm = -INFINITY;
+    bool bad = false;
+    for (int i = lane; i < static_cast<int>(C) * kWarps; i += 32) {
+      const float mi = __uint_as_float(pairs[i].x);
+      gm = fmaxf(gm, mi);
+      bad |= mi != mi;
     }
-    if ((!usable || empty) && rank == 0 && threadIdx.x == 0) atomicOr(P.err, RLK_DEVERR_PROBS);
-  } else {
-    int at = 0x7fffffff;
-    for (int i = lane; i < n; i += 32)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, o));
+    bad = __any_sync(kFull, bad);
+    int at = INT_MAX;
+    for (int i = lane; i < static_cast<int>(C) * kWarps; i += 32)
       if (__uint_as_float(pairs[i].x) == gm) at = min(at, static_cast<int>(pairs[i].y));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      at = min(at, __shfl_xor_sync(kFull, at, o));
-      bad += __shfl_xor_sync(kFull, bad, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
     const bool empty = gm == -INFINITY;
-    for (int64_t i = i0; i < P.V; i += step)
-      store_as(p + i, bad != 0.f ? NAN : (i == at && !empty) ? 1.f : 0.f);
-    if ((bad != 0.f || empty) && rank == 0 && threadIdx.x == 0) atomicOr(P.err, RLK_DEVERR_PROBS);
+    for (int i = t; i < n; i += kThreads)
+      store_as(p + i, bad ? NAN : (lo + i == at && !empty) ? 1.f : 0.f);
+    if ((bad || empty) && rank == 0 && t == 0) atomicOr(P.err, RLK_DEVERR_PROBS);
+    return;
   }
+
+  // this warp's numerators and their sum, relative to its maximum
+  float s = 0.f;
+  for (int b = 0; b < (kResident ? 1 : n); b += kStep) {
+    if (!kResident) load(b);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      v[j] = ex2_approx((v[j] - mref) * k);
+      s += v[j];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+  cluster_all_started();
+  if (lane < C)
+    st_cluster_v2(mapa_shared(smem_u32(&pairs[rank * kWarps + warp]), lane), __float_as_uint(m),
+                  __float_as_uint(s));
+  cluster_sync();
+  float gm = -INFINITY, S = 0.f;
+  for (int i = lane; i < static_cast<int>(C) * kWarps; i += 32)
+    gm = fmaxf(gm, __uint_as_float(pairs[i].x));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, o));
+  const float gref = gm == -INFINITY ? 0.f : gm;
+  for (int i = lane; i < static_cast<int>(C) * kWarps; i += 32)
+    S += __uint_as_float(pairs[i].y) * ex2_approx((__uint_as_float(pairs[i].x) - gref) * k);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(kFull, S, o);
+  // nothing left by the mask: all zeros; a NaN or +inf logit, or a temperature
+  // that is not a positive finite number: all NaN
+  const bool usable = tau > 0.f && k > 0.f && k < INFINITY && S == S;
+  const bool empty = usable && gm == -INFINITY;
+  float f = ex2_approx((mref - gref) * k) / S;
+  if (m == -INFINITY || empty) f = 0.f;
+  if (!usable) f = NAN;
+  for (int b = 0; b < (kResident ? 1 : n); b += kStep) {
+    if (!kResident) {
+      load(b);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) v[j] = ex2_approx((v[j] - mref) * k);
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      if (t < n - b - j * kThreads) store_as(p + b + t + j * kThreads, v[j] * f);
+  }
+  if ((!usable || empty) && rank == 0 && t == 0) atomicOr(P.err, RLK_DEVERR_PROBS);
 }
 
 // =====================================================================
@@ -231,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) probs_kernel(const ProbArgs P) {
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerMaxCluster = 8;
-constexpr int kVerUnroll = 8;
+constexpr int kVerUnroll = 10;
 constexpr int kVerPiece = 1024;  // elements walked at a time: 32 consecutive ones per lane
 
 struct VerifyArgs {
@@ -243,6 +232,7 @@ struct VerifyArgs {
   const float* us;
   const int64_t* lens;
   int64_t K, V;
+  int seg;  // entries per warp, a multiple of 32
   int64_t* tokens;
   int64_t* accepted;
   unsigned* err;
@@ -254,7 +244,7 @@ __device__ __forceinline__ double residual(float p, float q) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs P) {
+__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs P) {
   __shared__ double totals[2][kVerMaxCluster * kVerWarps];
   __shared__ double walk[32 * 33];
   __shared__ int s_n;
@@ -302,31 +292,48 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs P)
   const int n = s_n;
   const T* p = pb + n * P.p_sk;
   const T* q = n < len && P.q ? qb + n * P.q_sk : nullptr;
-  const int64_t hot = n < len && !P.q ? drafts[n] : -1;  // where q is one
+  // where q is one; a draft outside [0, V) is nowhere
+  const int64_t drafted = n < len && !P.q ? drafts[n] : -1;
+  const int hot = drafted >= 0 && drafted < P.V ? static_cast<int>(drafted) : -1;
 
   // this warp's segment
-  const int64_t nseg = static_cast<int64_t>(C) * kVerWarps;
-  const int64_t seg = ((P.V + nseg - 1) / nseg + 31) / 32 * 32;
+  const int nseg = static_cast<int>(C) * kVerWarps;
   const int my = static_cast<int>(rank) * kVerWarps + warp;
-  const int64_t lo = min(my * seg, P.V), hi = min(lo + seg, P.V);
+  const int V = static_cast<int>(P.V);
+  const int lo = static_cast<int>(min(static_cast<int64_t>(my) * P.seg, P.V));
+  const int hi = lo + min(P.seg, V - lo);
 
   for (int attempt = 0;; ++attempt) {
     const bool sub = attempt == 0;  // the second time p alone
-    auto value = [&](int64_t i) -> double {
+    auto value = [&](int i) -> double {
       const float qv = sub ? (q ? to_f32(q[i]) : i == hot ? 1.f : 0.f) : 0.f;
       return residual(to_f32(p[i]), qv);
     };
+    // one round trip for every 2 kVerUnroll elements of a lane: the loads of a
+    // round do not wait for anything but the row's number
     double acc = 0.;
-    for (int64_t i0 = lo + lane; i0 < hi; i0 += 32 * kVerUnroll) {
-      float pv[kVerUnroll], qv[kVerUnroll];
+    if (sub && q) {
+      for (int i = lo + lane; i < hi; i += 32 * kVerUnroll) {
+        float pv[kVerUnroll], qv[kVerUnroll];
 #pragma unroll
-      for (int j = 0; j < kVerUnroll; ++j) {
-        const int64_t i = i0 + 32 * j;
-        pv[j] = i < hi ? to_f32(p[i]) : 0.f;
-        qv[j] = i < hi && sub ? (q ? to_f32(q[i]) : i == hot ? 1.f : 0.f) : 0.f;
+        for (int j = 0; j < kVerUnroll; ++j) {
+          const bool in = i < hi - 32 * j;
+          pv[j] = in ? to_f32(p[i + 32 * j]) : 0.f;
+          qv[j] = in ? to_f32(q[i + 32 * j]) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kVerUnroll; ++j) acc += residual(pv[j], qv[j]);
       }
+    } else {
+      const int h = sub ? hot : -1;
+      for (int i = lo + lane; i < hi; i += 32 * 2 * kVerUnroll) {
+        float pv[2 * kVerUnroll];
 #pragma unroll
-      for (int j = 0; j < kVerUnroll; ++j) acc += residual(pv[j], qv[j]);
+        for (int j = 0; j < 2 * kVerUnroll; ++j) pv[j] = i < hi - 32 * j ? to_f32(p[i + 32 * j]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 2 * kVerUnroll; ++j)
+          acc += residual(pv[j], i + 32 * j == h ? 1.f : 0.f);
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
@@ -389,13 +396,13 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs P)
     if (found != my) return;
 
     // the owner walks its segment in order
-    int64_t fallback = -1, token = -1;
-    for (int64_t i0 = lo; i0 < hi && token < 0; i0 += kVerPiece) {
+    int fallback = -1, token = -1;
+    for (int i0 = lo; i0 < hi && token < 0; i0 += kVerPiece) {
       __syncwarp();
 #pragma unroll 8
       for (int j = 0; j < 32; ++j) {
-        const int64_t i = i0 + j * 32 + lane;
-        walk[j * 33 + lane] = i < hi ? value(i) : 0.;
+        const int i = i0 + j * 32 + lane;
+        walk[j * 33 + lane] = j * 32 + lane < hi - i0 ? value(i) : 0.;
       }
       __syncwarp();
       const double* w = walk + lane * 33;
@@ -464,17 +471,25 @@ rlk_status launch_clusters(void (*kern)(Args), const Args& a, int64_t groups, in
   return RLK_OK;
 }
 
-// The register plan of a V-entry row: the smallest of three per-thread counts
-// and of the clusters of 1, 2, 4 and 8 CTAs that holds it.
+template <typename TIn, typename TOut, int kThreads, int kN, int kBlocks, bool kResident>
+rlk_status launch_probs_as(ProbArgs a, int64_t R, int C, cudaStream_t st) {
+  a.slice = (a.V - 1) / C / 32 * 32 + 32;  // V / C rounded up to whole warps
+  return launch_clusters(probs_kernel<TIn, TOut, kThreads, kN, kBlocks, kResident>, a, R, C,
+                         kThreads, st);
+}
+
+// The register plan of a V-entry row: 16 entries per thread on the smallest
+// cluster that holds it (several small CTAs share an SM, so that one's loads run
+// beside another's stores), more per thread where eight CTAs do not.
 template <typename TIn, typename TOut>
 rlk_status launch_probs(const ProbArgs& a, int64_t R, cudaStream_t st) {
-  const int64_t V = a.V;
-  if (V <= 2048) return launch_clusters(probs_kernel<TIn, TOut, 256, 8, true>, a, R, 1, 256, st);
-  if (V <= 8192) return launch_clusters(probs_kernel<TIn, TOut, 512, 16, true>, a, R, 1, 512, st);
+  const int V = a.V;
+  if (V <= 2048) return launch_probs_as<TIn, TOut, 256, 8, 4, true>(a, R, 1, st);
   for (int C = 1; C <= kProbMaxCluster; C *= 2)
-    if (V <= C * 512 * 40)
-      return launch_clusters(probs_kernel<TIn, TOut, 512, 40, true>, a, R, C, 512, st);
-  return launch_clusters(probs_kernel<TIn, TOut, 512, 16, false>, a, R, kProbMaxCluster, 512, st);
+    if (V <= C * 512 * 16) return launch_probs_as<TIn, TOut, 512, 16, 3, true>(a, R, C, st);
+  if (V <= 8 * 512 * 24) return launch_probs_as<TIn, TOut, 512, 24, 2, true>(a, R, 8, st);
+  if (V <= 8 * 512 * 40) return launch_probs_as<TIn, TOut, 512, 40, 2, true>(a, R, 8, st);
+  return launch_probs_as<TIn, TOut, 512, 16, 3, false>(a, R, 8, st);
 }
 
 }  // namespace
@@ -514,7 +529,7 @@ extern "C" rlk_status rlk_token_probs(const void* logits, int logits_type, int64
   a.row_tau = row_temperature;
   a.ldx = ld_logits;
   a.ldp = ld_probs;
-  a.V = V;
+  a.V = static_cast<int>(V);
   a.tau = temperature;
   a.err = static_cast<unsigned*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -570,6 +585,7 @@ extern "C" rlk_status rlk_draft_verify(const void* target_probs, int64_t target_
   a.accepted = num_accepted;
   a.err = static_cast<unsigned*>(workspace);
   const int C = V <= 4096 ? 1 : V <= 16384 ? 2 : V <= 65536 ? 4 : 8;
+  a.seg = static_cast<int>((V - 1) / (C * kVerWarps) / 32 * 32 + 32);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return probs_type == RLK_TYPE_F32
              ? launch_clusters(verify_kernel<float>, a, B, C, kVerThreads, st)
