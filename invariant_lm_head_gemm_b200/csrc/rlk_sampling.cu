@@ -10,6 +10,8 @@
 // row alignment (an odd V puts every row at another offset) and keeps the
 // element-to-thread map, and with it the order of the sums, the same for all
 // rows.
+#include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -53,150 +55,398 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_
 // p[v] = 2^((x[v] - m) k) / S,  k = log2(e) / tau,  m = max x,  S = sum of the
 // numerators; tau = 0 puts 1 at the first maximum.
 //
-// Each thread keeps its elements in registers (kN of them, all loads in flight
-// at once), so a row is read once.  Each warp takes its own maximum m_w and its
-// sum relative to m_w; the pairs (m_w, s_w) of all warps of the cluster meet in
-// every CTA's shared memory, one cluster barrier later every warp folds them in
-// the same order, and the numerators already in registers need one more
-// factor, 2^((m_w - m) k) / S.  Rows beyond the registers of eight CTAs
-// (kResident = false) are read twice, the numerators formed again.
-constexpr int kProbMaxWarps = 16;
+// A row belongs to a cluster of 1, 2, 4 or 8 CTAs, by V and the type alone: the
+// fewest whose shared memory holds it at two CTAs per SM.  A CTA copies its slice
+// in (16-byte asynchronous copies; a slice that starts off a 16-byte boundary sits
+// as far off in shared memory) and looks at it three times: its maximum, its sum
+// relative to that, and, when the slices' pairs (maximum, sum) have met, the
+// probabilities.  The sum takes entries by their place in the slice, whatever the
+// slice's alignment, so its order is the same for every row; the other two looks
+// take whole aligned vectors.
+//
+// Bound by HBM where there are many rows: each entry is read once and written
+// once, one CTA's copies running beside the other's looks.  Few instructions per
+// entry is what that takes: holding the entries in registers instead (one look,
+// one exponential, but 64 warps to a row of 50257, each with its reductions) ran
+// 55 instructions per entry and 128 us at 1027 x 50257 bf16.
 constexpr int kProbMaxCluster = 8;
+constexpr int kProbThreads = 256;
+constexpr uint32_t kProbSlice = 100u * 1024u;  // bytes of a slice at most
+constexpr uint32_t kProbPad = 48u;             // room for an offset and whole vectors behind
 
 struct ProbArgs {
   const void* x;
   void* p;
   const float* row_tau;
   int64_t ldx, ldp;
+  int64_t R;
   int V;
   int slice;  // entries per CTA of the cluster
   float tau;
   unsigned* err;
 };
 
-template <typename TIn, typename TOut, int kThreads, int kN, int kBlocks, bool kResident>
-__global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const ProbArgs P) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// What every warp folds from the pairs of a row: its maximum and S (or, greedy,
+// the least index of the maximum).
+struct RowStats {
+  float m, S;
+  int at;
+  bool nan;
+};
+
+__device__ __forceinline__ RowStats fold_pairs(const uint2* pairs, int n, float k, bool greedy,
+                                               int lane) {
+  RowStats r{-INFINITY, 0.f, INT_MAX, false};
+  for (int i = lane; i < n; i += 32) {
+    const float mi = __uint_as_float(pairs[i].x);
+    r.m = fmaxf(r.m, mi);
+    r.nan |= mi != mi;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(kFull, r.m, o));
+  if (greedy) {
+    r.nan = __any_sync(kFull, r.nan);
+    for (int i = lane; i < n; i += 32)
+      if (__uint_as_float(pairs[i].x) == r.m) r.at = min(r.at, static_cast<int>(pairs[i].y));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) r.at = min(r.at, __shfl_xor_sync(kFull, r.at, o));
+    return r;
+  }
+  const float ref = r.m == -INFINITY ? 0.f : r.m;  // -inf - -inf would be NaN
+  for (int i = lane; i < n; i += 32)
+    r.S += __uint_as_float(pairs[i].y) * ex2_approx((__uint_as_float(pairs[i].x) - ref) * k);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.S += __shfl_xor_sync(kFull, r.S, o);
+  return r;
+}
+
+// A row's probabilities from its logits; greedy rows are `inv` (0 or NaN) but at
+// one place.
+struct RowOut {
+  float ref, k, inv;
+  int at;  // greedy: where the one is (-1: nowhere)
+  __device__ __forceinline__ float operator()(float x) const { return ex2_approx((x - ref) * k) * inv; }
+  __device__ __forceinline__ float at_place(int i) const { return i == at ? 1.f : inv; }
+};
+
+// Sets `bad` where the row gives no distribution: nothing left by its mask
+// (zeros), or a NaN, +inf, or a temperature that is not a positive finite number
+// (NaN).
+__device__ __forceinline__ RowOut row_out(const RowStats& r, float tau, float k, bool greedy,
+                                          bool& bad) {
+  RowOut o;
+  o.k = k;
+  o.ref = r.m == -INFINITY ? 0.f : r.m;
+  const bool empty = r.m == -INFINITY;
+  const bool usable = greedy ? !r.nan : tau > 0.f && k > 0.f && k < INFINITY && r.S == r.S;
+  o.inv = !usable ? NAN : empty || greedy ? 0.f : 1.f / r.S;
+  o.at = empty || !usable ? -1 : r.at;
+  bad = !usable || empty;
+  return o;
+}
+
+// 2^(x k - c) or, where c = ref k is not finite, 2^((x - ref) k).  The rounding of
+// c is common to all entries and to their sum, and cancels between them.
+struct RowExp {
+  float k, ref, c;
+  bool plain;
+  __device__ __forceinline__ RowExp(float m, float kk) {
+    k = kk;
+    ref = m == -INFINITY ? 0.f : m;  // -inf - -inf would be NaN
+    c = ref * k;
+    plain = fabsf(c) < 1e30f;
+  }
+  // for one maximum's numerators seen from another's
+  __device__ __forceinline__ float shift(const RowExp& to) const {
+    return plain && to.plain ? ex2_approx(c - to.c) : ex2_approx((ref - to.ref) * k);
+  }
+};
+
+template <typename T, int kThreads>
+struct Slice {
+  static constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // entries per 16 bytes
+  static constexpr int kPair = sizeof(T) == 2 ? 2 : 1;
+  // largest entry of `nv` aligned vectors
+  static __device__ __forceinline__ float maximum(const T* room, int nv) {
+    const uint4* src = reinterpret_cast<const uint4*>(room);
+    if constexpr (kPair == 1) {
+      float m = -INFINITY;
+#pragma unroll 4
+      for (int i = threadIdx.x; i < nv; i += kThreads) {
+        const uint4 q = src[i];
+        m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(q.x), __uint_as_float(q.y))),
+                  fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+      }
+      return m;
+    } else {
+      __nv_bfloat162 m = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+#pragma unroll 4
+      for (int i = threadIdx.x; i < nv; i += kThreads) {
+        const uint4 q = src[i];
+        const __nv_bfloat162 a = __hmax2(as2(q.x), as2(q.y)), b = __hmax2(as2(q.z), as2(q.w));
+        m = __hmax2(m, __hmax2(a, b));
+      }
+      return fmaxf(__low2float(m), __high2float(m));
+    }
+  }
+  // sum of f over the n entries at buf = room + off, by their place
+  template <typename F>
+  static __device__ __forceinline__ float sum(const T* buf, int off, int n, F f) {
+    float s = 0.f;
+    if constexpr (kPair == 1) {
+#pragma unroll 8
+      for (int i = threadIdx.x; i < n; i += kThreads) s += f(to_f32(buf[i]));
+    } else {
+      // pairs of neighbours; at an odd offset a pair straddles two words
+      const int np = (n + 1) >> 1;  // the entry behind an odd n is -inf
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(buf - (off & 1));
+      if (off & 1) {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < np; i += kThreads)
+          s = add(s, __funnelshift_r(w[i], w[i + 1], 16), f);
+      } else {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < np; i += kThreads) s = add(s, w[i], f);
+      }
+    }
+    return s;
+  }
+  template <typename F>
+  static __device__ __forceinline__ float add(float s, uint32_t x, F f) {
+    s += f(__uint_as_float(x << 16));
+    return s + f(__uint_as_float(x & 0xffff0000u));
+  }
+  static __device__ __forceinline__ __nv_bfloat162 as2(uint32_t u) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&u);
+  }
+  // p = f of the n entries
+  template <typename TOut, typename F>
+  static __device__ __forceinline__ void write(TOut* p, const T* room, int off, int n, F f) {
+    const T* buf = room + off;
+    if (sizeof(T) == sizeof(TOut) &&
+        (reinterpret_cast<uintptr_t>(p) & 15u) == off * sizeof(T)) {
+      // the same place within 16 bytes: whole vectors, but at the ends
+      const int head = min(n, (kVec - off) & (kVec - 1));
+      const int nv = (n - head) / kVec;
+      const uint4* src = reinterpret_cast<const uint4*>(buf + head);
+      uint4* dst = reinterpret_cast<uint4*>(p + head);
+#pragma unroll 4
+      for (int i = threadIdx.x; i < nv; i += kThreads) {
+        const uint4 q = src[i];
+        dst[i] = make_uint4(word(q.x, f), word(q.y, f), word(q.z, f), word(q.w, f));
+      }
+      const int t = threadIdx.x, tail = head + nv * kVec;
+      if (t < head) store_as(p + t, f(to_f32(buf[t])));
+      if (t < n - tail) store_as(p + tail + t, f(to_f32(buf[tail + t])));
+    } else {
+#pragma unroll 8
+      for (int i = threadIdx.x; i < n; i += kThreads) store_as(p + i, f(to_f32(buf[i])));
+    }
+  }
+  template <typename F>
+  static __device__ __forceinline__ uint32_t word(uint32_t x, F f) {
+    if constexpr (kPair == 1) {
+      return __float_as_uint(f(__uint_as_float(x)));
+    } else {
+      const __nv_bfloat162 b =
+          __floats2bfloat162_rn(f(__uint_as_float(x << 16)), f(__uint_as_float(x & 0xffff0000u)));
+      return *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+};
+
+template <typename TIn, typename TOut, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 4) probs_kernel(const ProbArgs P) {
+  using S = Slice<TIn, kThreads>;
   constexpr int kWarps = kThreads / 32;
-  constexpr int kStep = kN * kThreads;
-  __shared__ uint2 pairs[kProbMaxCluster * kProbMaxWarps];
+  constexpr int kVec = S::kVec;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float warp_max[kWarps], warp_sum[kWarps];
+  __shared__ int warp_at[kWarps];
+  __shared__ uint2 met[kProbMaxCluster];
+  TIn* room = reinterpret_cast<TIn*>(smem);
+  uint32_t C, rank;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  if (C > 1) cluster_started();
+  const int64_t row = blockIdx.x / C;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int lo = static_cast<int>(min(static_cast<int64_t>(rank) * P.slice, static_cast<int64_t>(P.V)));
+  const int n = min(P.slice, P.V - lo);  // this CTA's entries
+  // the slice, and -inf around it up to whole vectors
+  const TIn* g = static_cast<const TIn*>(P.x) + row * P.ldx + lo;
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / sizeof(TIn));
+  const int nv = (off + n + kVec) / kVec;  // vectors, one entry more than the slice at least
+  {
+    const int head = min(n, (kVec - off) & (kVec - 1));
+    const int whole = (n - head) / kVec;
+    const uint32_t dst = smem_u32(room + off + head);
+    for (int i = t; i < whole; i += kThreads) cp_async16(dst + i * 16, g + head + i * kVec);
+    const int tail = head + whole * kVec;
+    if (t < head) room[off + t] = g[t];
+    if (t < n - tail) room[off + tail + t] = g[tail + t];
+    if (t < off) store_as(room + t, -INFINITY);
+    if (t < nv * kVec - off - n) store_as(room + off + n + t, -INFINITY);
+  }
+  const float tau = P.row_tau ? P.row_tau[row] : P.tau;
+  const float k = kSampLog2e / tau;
+  const bool greedy = tau == 0.f;
+  cp_async_wait_all();
+  __syncthreads();
+
+  float m = S::maximum(room, nv);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  if (lane == 0) warp_max[warp] = m;
+  __syncthreads();
+  m = warp_max[lane & (kWarps - 1)];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+
+  const RowExp e(m, k);
+  const TIn* buf = room + off;
+  float s = 0.f;
+  int at = INT_MAX;
+  if (greedy) {  // the first maximum; a NaN makes the sum one
+    for (int i = t; i < n; i += kThreads) {
+      const float x = to_f32(buf[i]);
+      if (x != x) s = NAN;
+      if (x == m) at = min(at, lo + i);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
+    if (lane == 0) warp_at[warp] = at;
+  } else if (e.plain) {
+    s = S::sum(buf, off, n, [&](float x) { return ex2_approx(fmaf(x, e.k, -e.c)); });
+  } else {
+    s = S::sum(buf, off, n, [&](float x) { return ex2_approx((x - e.ref) * e.k); });
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+  if (lane == 0) warp_sum[warp] = s;
+  __syncthreads();
+  s = warp_sum[lane & (kWarps - 1)];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+  if (greedy) {
+    at = warp_at[lane & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
+  }
+  if (C > 1) {
+    // the slices' maxima and sums (or, greedy, the places; NaN as the maximum)
+    cluster_all_started();
+    if (warp == 0 && lane < C)
+      st_cluster_v2(mapa_shared(smem_u32(&met[rank]), lane),
+                    __float_as_uint(greedy && s != s ? NAN : m),
+                    greedy ? static_cast<uint32_t>(at) : __float_as_uint(s));
+    cluster_sync();
+    float gm = -INFINITY;
+    for (int i = 0; i < static_cast<int>(C); ++i) gm = fmaxf(gm, __uint_as_float(met[i].x));
+    const RowExp all(gm, k);
+    s = 0.f;
+    at = INT_MAX;
+    for (int i = 0; i < static_cast<int>(C); ++i) {
+      const float mi = __uint_as_float(met[i].x);
+      if (greedy) {
+        if (mi != mi) s = NAN;
+        if (mi == gm) at = min(at, static_cast<int>(met[i].y));
+      } else if (mi != -INFINITY || __uint_as_float(met[i].y) != 0.f) {
+        s += __uint_as_float(met[i].y) * RowExp(mi, k).shift(all);
+      }
+    }
+    m = gm;
+  }
+
+  // a row that gives no distribution: nothing left by its mask (zeros), or a NaN,
+  // +inf, or a temperature that is not a positive finite number (NaN)
+  const bool usable = s == s && (greedy || (tau > 0.f && k > 0.f && k < INFINITY));
+  const bool empty = m == -INFINITY;
+  if ((!usable || empty) && rank == 0 && t == 0) atomicOr(P.err, RLK_DEVERR_PROBS);
+  TOut* p = static_cast<TOut*>(P.p) + row * P.ldp + lo;
+  if (!usable || empty || greedy) {
+    const float rest = usable ? 0.f : NAN;
+    if (!usable || empty) at = -1;
+#pragma unroll 8
+    for (int i = t; i < n; i += kThreads) store_as(p + i, lo + i == at ? 1.f : rest);
+  } else {
+    const RowExp o(m, k);
+    const float inv = 1.f / s;
+    if (o.plain) {
+      S::write(p, room, off, n, [&](float x) { return ex2_approx(fmaf(x, o.k, -o.c)) * inv; });
+    } else {
+      S::write(p, room, off, n, [&](float x) { return ex2_approx((x - o.ref) * o.k) * inv; });
+    }
+  }
+}
+
+// Rows that no cluster's shared memory holds: one CTA per row and eighth, its
+// entries read again from L2 or HBM for the second and third look.
+constexpr int kProbLongThreads = 512;
+constexpr int kProbLongWarps = kProbLongThreads / 32;
+
+template <typename TIn, typename TOut>
+__global__ void __launch_bounds__(kProbLongThreads) probs_long_kernel(const ProbArgs P) {
+  __shared__ uint2 pairs[kProbMaxCluster * kProbLongWarps];
   uint32_t C, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   cluster_started();
-  const int row = blockIdx.x / C;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x / C;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int lo = static_cast<int>(min(static_cast<int64_t>(rank) * P.slice, static_cast<int64_t>(P.V)));
-  const int n = min(P.slice, P.V - lo);  // this CTA's entries
-  const int t = threadIdx.x;
+  const int n = min(P.slice, P.V - lo);
   const TIn* x = static_cast<const TIn*>(P.x) + row * P.ldx + lo;
   TOut* p = static_cast<TOut*>(P.p) + row * P.ldp + lo;
-
-  float v[kN];
-  auto load = [&](int b) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] = t < n - b - j * kThreads ? to_f32(x[b + t + j * kThreads]) : -INFINITY;
-  };
-  float m = -INFINITY;
   const float tau = P.row_tau ? P.row_tau[row] : P.tau;
   const float k = kSampLog2e / tau;
   const bool greedy = tau == 0.f;
-  for (int b = 0; b < (kResident ? 1 : n); b += kStep) {
-    load(b);
-#pragma unroll
-    for (int j = 0; j < kN; ++j) m = fmaxf(m, v[j]);
-  }
+  float m = -INFINITY;
+#pragma unroll 16
+  for (int i = t; i < n; i += kProbLongThreads) m = fmaxf(m, to_f32(x[i]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  const float mref = m == -INFINITY ? 0.f : m;  // -inf - -inf would be NaN
-
+  const float ref = m == -INFINITY ? 0.f : m;
+  uint2 mine;
   if (greedy) {
-    // this warp's first maximum; a NaN travels as the maximum
     int first = INT_MAX;
     bool nan = false;
-    for (int b = 0; b < (kResident ? 1 : n); b += kStep) {
-      if (!kResident) load(b);
-#pragma unroll
-      for (int j = kN - 1; j >= 0; --j) {
-        const int i = b + t + j * kThreads;
-        nan |= v[j] != v[j];
-        if (i < n && v[j] == m) first = min(first, lo + i);
-      }
+#pragma unroll 16
+    for (int i = t; i < n; i += kProbLongThreads) {
+      const float v = to_f32(x[i]);
+      nan |= v != v;
+      if (v == m) first = min(first, lo + i);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(kFull, first, o));
     if (__any_sync(kFull, nan)) m = NAN;
-    cluster_all_started();
-    if (lane < C)
-      st_cluster_v2(mapa_shared(smem_u32(&pairs[rank * kWarps + warp]), lane), __float_as_uint(m),
-                    static_cast<uint32_t>(first));
-    cluster_sync();
-    float gm = -INFINITY;
-    bool bad = false;
-    for (int i = lane; i < static_cast<int>(C) * kWarps; i += 32) {
-      const float mi = __uint_as_float(pairs[i].x);
-      gm = fmaxf(gm, mi);
-      bad |= mi != mi;
-    }
+    mine = make_uint2(__float_as_uint(m), static_cast<uint32_t>(first));
+  } else {
+    float s = 0.f;
+#pragma unroll 16
+    for (int i = t; i < n; i += kProbLongThreads) s += ex2_approx((to_f32(x[i]) - ref) * k);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, o));
-    bad = __any_sync(kFull, bad);
-    int at = INT_MAX;
-    for (int i = lane; i < static_cast<int>(C) * kWarps; i += 32)
-      if (__uint_as_float(pairs[i].x) == gm) at = min(at, static_cast<int>(pairs[i].y));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
-    const bool empty = gm == -INFINITY;
-    for (int i = t; i < n; i += kThreads)
-      store_as(p + i, bad ? NAN : (lo + i == at && !empty) ? 1.f : 0.f);
-    if ((bad || empty) && rank == 0 && t == 0) atomicOr(P.err, RLK_DEVERR_PROBS);
-    return;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    mine = make_uint2(__float_as_uint(m), __float_as_uint(s));
   }
-
-  // this warp's numerators and their sum, relative to its maximum
-  float s = 0.f;
-  for (int b = 0; b < (kResident ? 1 : n); b += kStep) {
-    if (!kResident) load(b);
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      v[j] = ex2_approx((v[j] - mref) * k);
-      s += v[j];
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
   cluster_all_started();
   if (lane < C)
-    st_cluster_v2(mapa_shared(smem_u32(&pairs[rank * kWarps + warp]), lane), __float_as_uint(m),
-                  __float_as_uint(s));
+    st_cluster_v2(mapa_shared(smem_u32(&pairs[rank * kProbLongWarps + warp]), lane), mine.x, mine.y);
   cluster_sync();
-  float gm = -INFINITY, S = 0.f;
-  for (int i = lane; i < static_cast<int>(C) * kWarps; i += 32)
-    gm = fmaxf(gm, __uint_as_float(pairs[i].x));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, o));
-  const float gref = gm == -INFINITY ? 0.f : gm;
-  for (int i = lane; i < static_cast<int>(C) * kWarps; i += 32)
-    S += __uint_as_float(pairs[i].y) * ex2_approx((__uint_as_float(pairs[i].x) - gref) * k);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(kFull, S, o);
-  // nothing left by the mask: all zeros; a NaN or +inf logit, or a temperature
-  // that is not a positive finite number: all NaN
-  const bool usable = tau > 0.f && k > 0.f && k < INFINITY && S == S;
-  const bool empty = usable && gm == -INFINITY;
-  float f = ex2_approx((mref - gref) * k) / S;
-  if (m == -INFINITY || empty) f = 0.f;
-  if (!usable) f = NAN;
-  for (int b = 0; b < (kResident ? 1 : n); b += kStep) {
-    if (!kResident) {
-      load(b);
-#pragma unroll
-      for (int j = 0; j < kN; ++j) v[j] = ex2_approx((v[j] - mref) * k);
-    }
-#pragma unroll
-    for (int j = 0; j < kN; ++j)
-      if (t < n - b - j * kThreads) store_as(p + b + t + j * kThreads, v[j] * f);
-  }
-  if ((!usable || empty) && rank == 0 && t == 0) atomicOr(P.err, RLK_DEVERR_PROBS);
+  const RowStats rs = fold_pairs(pairs, static_cast<int>(C) * kProbLongWarps, k, greedy, lane);
+  bool bad;
+  const RowOut out = row_out(rs, tau, k, greedy, bad);
+  if (bad && rank == 0 && t == 0) atomicOr(P.err, RLK_DEVERR_PROBS);
+#pragma unroll 16
+  for (int i = t; i < n; i += kProbLongThreads)
+    store_as(p + i, greedy ? out.at_place(lo + i) : out(to_f32(x[i])));
 }
 
 // =====================================================================
@@ -213,15 +463,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const ProbArgs
 // tokens where the probabilities put them (in 32 bits they would move by more
 // than the smallest probabilities).
 //
-// The vocabulary is cut into C * kVerWarps contiguous segments, one per warp
-// of the cluster.  Pass 1 sums every segment; the totals meet in every CTA's
-// shared memory; every warp finds the segment that the threshold falls in, and
-// the warp that owns it walks it once more (from L2) in order.
+// The vocabulary is cut into at most kVerMaxSegs segments whose length follows
+// from V alone (256 entries up to V = 163840).  A warp sums a segment in a fixed
+// order, the totals meet in every CTA of the sequence's cluster, every warp finds
+// the segment that the threshold falls in by the same running sum, and the warp
+// that summed it walks it once more (from L2).  So a token does not depend on the
+// cluster's size, which follows the number of sequences.
+//
+// Bound by latency at few sequences (the drafts, their entries, the row, the
+// walk: four round trips and a cluster barrier) and by HBM at many.
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerMaxCluster = 8;
-constexpr int kVerUnroll = 10;
-constexpr int kVerPiece = 1024;  // elements walked at a time: 32 consecutive ones per lane
+constexpr int kVerPiece = 256;      // entries walked at a time: 8 consecutive ones per lane
+constexpr int kVerPer = 20;         // segments per lane of the running sum
+constexpr int kVerMaxSegs = 32 * kVerPer;
 
 struct VerifyArgs {
   const void* p;
@@ -231,22 +487,36 @@ struct VerifyArgs {
   const float* ua;
   const float* us;
   const int64_t* lens;
-  int64_t K, V;
-  int seg;  // entries per warp, a multiple of 32
+  int64_t K;
+  int V;
+  int seg;   // entries per segment, a multiple of kVerPiece
+  int nseg;
   int64_t* tokens;
   int64_t* accepted;
   unsigned* err;
 };
 
-__device__ __forceinline__ double residual(float p, float q) {
-  const double d = static_cast<double>(p) - static_cast<double>(q);
-  return d < 0. ? 0. : d;  // a NaN stays one
+// x 2^-896 in 64 bits, exactly: the exponent's field moved, not rebiased (a shift
+// and a mask, where converting takes the slow path of the conversion unit; zeros
+// and subnormals come out right by themselves).  Sums of such values, and their
+// comparison with a share of their own sum, need no scaling back.  An infinite x
+// becomes 2^-768, which kVerHuge tells from a sum of probabilities.
+__device__ __forceinline__ double scaled(float x) {
+  const int u = __float_as_int(x);
+  return __hiloint2double((u >> 3) & static_cast<int>(0x8fffffffu), u << 29);
+}
+constexpr double kVerHuge = 0x1p-769;
+
+// max(0, p - q), scaled; `bad` where it is NaN.
+__device__ __forceinline__ double residual(float p, float q, bool& bad) {
+  const float d = p - q;  // of the exact difference's sign
+  bad |= d != d;
+  return d > 0.f ? scaled(p) - scaled(q) : 0.;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs P) {
-  __shared__ double totals[2][kVerMaxCluster * kVerWarps];
-  __shared__ double walk[32 * 33];
+__global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel(const VerifyArgs P) {
+  __shared__ __align__(16) double totals[2][kVerMaxSegs];
   __shared__ int s_n;
   uint32_t C, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
@@ -257,102 +527,97 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   const T* pb = static_cast<const T*>(P.p) + b * P.p_sb;
   const T* qb = static_cast<const T*>(P.q) + (P.q ? b * P.q_sb : 0);
   const int64_t* drafts = P.drafts + b * P.K;
+  const int V = P.V;
+  const float us = P.us[b];
   int64_t len = P.lens ? P.lens[b] : P.K;
   len = len < 0 ? 0 : len > P.K ? P.K : len;
 
   if (warp == 0) {  // the acceptance tests, 32 drafts at a time
     int n = static_cast<int>(len);
     bool outside = false;
-    for (int64_t k0 = 0; k0 < len; k0 += 32) {
+    for (int64_t k0 = 0; k0 < P.K; k0 += 32) {
       const int64_t k = k0 + lane;
-      bool ok = true;
-      if (k < len) {
-        const int64_t d = drafts[k];
-        const double u = P.ua[b * P.K + k];
-        ok = d >= 0 && d < P.V;
+      // what lies behind the length is loaded (it is there) but not looked at
+      const int64_t d = k < P.K ? drafts[k] : 0;
+      const double u = k < P.K ? P.ua[b * P.K + k] : 0.f;
+      bool ok = k >= len;
+      if (!ok && d >= 0 && d < V) {
+        const double pd = to_f32(pb[k * P.p_sk + d]);
+        const double qd = P.q ? static_cast<double>(to_f32(qb[k * P.q_sk + d])) : 1.;
+        ok = u * qd < pd;
+      } else {
         outside |= !ok;
-        if (ok) {
-          const double pd = to_f32(pb[k * P.p_sk + d]);
-          const double qd = P.q ? static_cast<double>(to_f32(qb[k * P.q_sk + d])) : 1.;
-          ok = u * qd < pd;
-        }
       }
       const uint32_t no = __ballot_sync(kFull, !ok);
       if (no && n == static_cast<int>(len)) n = static_cast<int>(k0) + __ffs(no) - 1;
+      if (rank == 0 && k < P.K && k < n) P.tokens[b * (P.K + 1) + k] = d;
     }
     if (__any_sync(kFull, outside) && lane == 0 && rank == 0) atomicOr(P.err, RLK_DEVERR_TARGET);
     if (lane == 0) s_n = n;
-    if (rank == 0) {
-      for (int64_t k = lane; k <= P.K; k += 32)
-        if (k != n) P.tokens[b * (P.K + 1) + k] = k < n ? drafts[k] : -1;
-      if (lane == 0) P.accepted[b] = n;
-    }
+  } else {
+    for (int i = P.nseg + threadIdx.x - 32; i < kVerMaxSegs; i += kVerThreads - 32)
+      totals[0][i] = totals[1][i] = 0.;
   }
   __syncthreads();
   const int n = s_n;
+  if (warp == 1 && rank == 0) {
+    for (int64_t k = n + 1 + lane; k <= P.K; k += 32) P.tokens[b * (P.K + 1) + k] = -1;
+    if (lane == 0) P.accepted[b] = n;
+  }
   const T* p = pb + n * P.p_sk;
   const T* q = n < len && P.q ? qb + n * P.q_sk : nullptr;
   // where q is one; a draft outside [0, V) is nowhere
   const int64_t drafted = n < len && !P.q ? drafts[n] : -1;
-  const int hot = drafted >= 0 && drafted < P.V ? static_cast<int>(drafted) : -1;
-
-  // this warp's segment
-  const int nseg = static_cast<int>(C) * kVerWarps;
-  const int my = static_cast<int>(rank) * kVerWarps + warp;
-  const int V = static_cast<int>(P.V);
-  const int lo = static_cast<int>(min(static_cast<int64_t>(my) * P.seg, P.V));
-  const int hi = lo + min(P.seg, V - lo);
+  int hot = drafted >= 0 && drafted < V ? static_cast<int>(drafted) : -1;
+  const int nw = static_cast<int>(C) * kVerWarps;
+  const int my = static_cast<int>(rank) * kVerWarps + warp;  // segments my, my + nw, ...
 
   for (int attempt = 0;; ++attempt) {
-    const bool sub = attempt == 0;  // the second time p alone
-    auto value = [&](int i) -> double {
-      const float qv = sub ? (q ? to_f32(q[i]) : i == hot ? 1.f : 0.f) : 0.f;
-      return residual(to_f32(p[i]), qv);
+    // the residual of 8 entries, i + step j, as far as `left` goes
+    bool bad = false;
+    auto add8 = [&](double acc, int i, int left) {
+      float pv[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) pv[j] = lane < left - 32 * j ? to_f32(p[i + 32 * j]) : 0.f;
+      if (q) {
+        float qv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) qv[j] = lane < left - 32 * j ? to_f32(q[i + 32 * j]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc += residual(pv[j], qv[j], bad);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc += residual(pv[j], i + 32 * j == hot ? 1.f : 0.f, bad);
+      }
+      return acc;
     };
-    // one round trip for every 2 kVerUnroll elements of a lane: the loads of a
-    // round do not wait for anything but the row's number
-    double acc = 0.;
-    if (sub && q) {
-      for (int i = lo + lane; i < hi; i += 32 * kVerUnroll) {
-        float pv[kVerUnroll], qv[kVerUnroll];
+    if (attempt == 0) cluster_all_started();
+    for (int s = my; s < P.nseg; s += nw) {
+      const int lo = s * P.seg, size = min(P.seg, V - lo);
+      double acc = 0.;
+      for (int o = 0; o < size; o += kVerPiece) acc = add8(acc, lo + o + lane, size - o);
 #pragma unroll
-        for (int j = 0; j < kVerUnroll; ++j) {
-          const bool in = i < hi - 32 * j;
-          pv[j] = in ? to_f32(p[i + 32 * j]) : 0.f;
-          qv[j] = in ? to_f32(q[i + 32 * j]) : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < kVerUnroll; ++j) acc += residual(pv[j], qv[j]);
-      }
-    } else {
-      const int h = sub ? hot : -1;
-      for (int i = lo + lane; i < hi; i += 32 * 2 * kVerUnroll) {
-        float pv[2 * kVerUnroll];
-#pragma unroll
-        for (int j = 0; j < 2 * kVerUnroll; ++j) pv[j] = i < hi - 32 * j ? to_f32(p[i + 32 * j]) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 2 * kVerUnroll; ++j)
-          acc += residual(pv[j], i + 32 * j == h ? 1.f : 0.f);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
-    if (sub) cluster_all_started();
-    if (lane < C) {
-      const uint32_t to = mapa_shared(smem_u32(&totals[attempt][my]), lane);
-      st_cluster_v2(to, static_cast<uint32_t>(__double2loint(acc)),
-                    static_cast<uint32_t>(__double2hiint(acc)));
+      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
+      if (__any_sync(kFull, bad)) acc = static_cast<double>(NAN);
+      if (lane < C)
+        st_cluster_v2(mapa_shared(smem_u32(&totals[attempt][s]), lane),
+                      static_cast<uint32_t>(__double2loint(acc)),
+                      static_cast<uint32_t>(__double2hiint(acc)));
     }
     cluster_sync();
 
-    // every warp: the running sums over the segments, four of them per lane
-    constexpr int kPer = kVerMaxCluster * kVerWarps / 32;
-    double t[kPer], own = 0.;
+    // every warp: the running sum over lanes' segments, kVerPer of them per lane
+    const double* tot = totals[attempt] + lane * kVerPer;
+    double t[kVerPer / 2];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      t[j] = lane * kPer + j < nseg ? totals[attempt][lane * kPer + j] : 0.;
-      own += t[j];
+    for (int j = 0; j < kVerPer / 2; ++j) {
+      const double2 two = *reinterpret_cast<const double2*>(tot + 2 * j);
+      t[j] = two.x + two.y;
     }
+#pragma unroll
+    for (int j = 0; j < kVerPer / 4; ++j) t[j] += t[j + kVerPer / 4];
+    const double own = (t[0] + t[1]) + (t[2] + t[3]) + t[4];
+    static_assert(kVerPer == 20, "the sum above");
     double incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -360,100 +625,99 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
       if (lane >= o) incl += up;
     }
     const double S = __shfl_sync(kFull, incl, 31);
-    double excl = __shfl_up_sync(kFull, incl, 1);
-    if (lane == 0) excl = 0.;
-    if (S == 0. && attempt == 0 && n < len) continue;  // p <= q everywhere: take p
-    const bool good = S > 0. && S < static_cast<double>(INFINITY);
-    if (!good) {
+    if (S == 0. && attempt == 0 && n < len) {  // p <= q everywhere: take p
+      q = nullptr;
+      hot = -1;
+      continue;
+    }
+    if (!(S > 0. && S < kVerHuge)) {
       if (rank == 0 && threadIdx.x == 0) {
         P.tokens[b * (P.K + 1) + n] = -1;
         atomicOr(P.err, RLK_DEVERR_PROBS);
       }
       return;  // every warp of the cluster alike
     }
-    const double c = static_cast<double>(P.us[b]) * S;
-    int found = 0x7fffffff, last = -1;
-    double before = 0., run = excl;
+    // the lane, then its segment, in which the running sum passes c; the last of
+    // positive residual for us >= 1 (or NaN), or should rounding leave none
+    const double c = us < 1.f ? static_cast<double>(us) * S : static_cast<double>(INFINITY);
+    auto first_or_last = [&](bool over, bool positive) {
+      const uint32_t first = __ballot_sync(kFull, over && positive);
+      const uint32_t any = __ballot_sync(kFull, positive);
+      return first ? __ffs(first) - 1 : 31 - __clz(any);
+    };
+    const int l = first_or_last(incl > c, own > 0.);
+    double before = __shfl_up_sync(kFull, incl, 1);
+    before = l == 0 ? 0. : __shfl_sync(kFull, before, l);
+    const double x = lane < kVerPer ? totals[attempt][l * kVerPer + lane] : 0.;
+    double in = x;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (t[j] > 0. && run + t[j] > c && found == 0x7fffffff) {
-        found = lane * kPer + j;
-        before = run;
-      }
-      run += t[j];
-      if (t[j] > 0.) last = lane * kPer + j;
+    for (int o = 1; o < 32; o <<= 1) {
+      const double up = __shfl_up_sync(kFull, in, o);
+      if (lane >= o) in += up;
     }
-    const uint32_t who = __ballot_sync(kFull, found != 0x7fffffff);
-    // us >= 1 (or NaN): the last token of positive residual
-    const bool open = who == 0 || !(P.us[b] < 1.f);
-    if (!open) {
-      found = __shfl_sync(kFull, found, __ffs(who) - 1);
-      before = __shfl_sync(kFull, before, __ffs(who) - 1);
-    } else {
-      const uint32_t some = __ballot_sync(kFull, last >= 0);
-      found = __shfl_sync(kFull, last, 31 - __clz(some));
-    }
-    if (found != my) return;
+    const int j = first_or_last(before + in > c, x > 0.);
+    const double upto = __shfl_sync(kFull, in, (j + 31) & 31);  // of the segment before
+    if (j > 0) before += upto;
+    const int found = l * kVerPer + j;
+    if (found % nw != my) return;
 
-    // the owner walks its segment in order
-    int fallback = -1, token = -1;
-    for (int i0 = lo; i0 < hi && token < 0; i0 += kVerPiece) {
-      __syncwarp();
-#pragma unroll 8
-      for (int j = 0; j < 32; ++j) {
-        const int i = i0 + j * 32 + lane;
-        walk[j * 33 + lane] = j * 32 + lane < hi - i0 ? value(i) : 0.;
-      }
-      __syncwarp();
-      const double* w = walk + lane * 33;
-      double sum = 0.;
-      int lastpos = -1;
-#pragma unroll 8
-      for (int j = 0; j < 32; ++j) {
-        sum += w[j];
-        if (w[j] > 0.) lastpos = j;
-      }
-      double in = sum;
+    // the segment's warp walks it, 8 consecutive entries per lane
+    const int lo = found * P.seg, size = min(P.seg, V - lo);
+    int token = -1;
+    bool sure = false;
+    for (int o = 0; o < size && !sure; o += kVerPiece) {
+      const int i = lo + o + lane * 8, left = size - o - lane * 8;
+      double w[8];
+      float pv[8], qv[8];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(kFull, in, o);
-        if (lane >= o) in += up;
+      for (int k = 0; k < 8; ++k) pv[k] = k < left ? to_f32(p[i + k]) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        qv[k] = k < left && q ? to_f32(q[i + k]) : i + k == hot ? 1.f : 0.f;
+      int last = -1;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const double r = residual(pv[k], qv[k], bad);
+        if (r > 0.) last = k;
+        w[k] = k == 0 ? r : w[k > 0 ? k - 1 : 0] + r;
       }
-      double ex = __shfl_up_sync(kFull, in, 1);
-      if (lane == 0) ex = 0.;
-      const uint32_t cross = __ballot_sync(kFull, !open && lastpos >= 0 && before + in > c);
-      const uint32_t pos = __ballot_sync(kFull, lastpos >= 0);
-      if (cross) {
-        const int l = __ffs(cross) - 1;
-        int at = lastpos;  // rounding may leave the walk a hair below the sum
-        if (lane == l) {
-          double r = before + ex;
-          for (int j = 0; j < 32; ++j) {
-            r += w[j];
-            if (w[j] > 0. && r > c) {
-              at = j;
-              break;
-            }
-          }
+      double sum = w[7];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double up = __shfl_up_sync(kFull, sum, d);
+        if (lane >= d) sum += up;
+      }
+      double base = __shfl_up_sync(kFull, sum, 1);
+      base = before + (lane == 0 ? 0. : base);
+      const uint32_t cross = __ballot_sync(kFull, last >= 0 && before + sum > c);
+      const uint32_t pos = __ballot_sync(kFull, last >= 0);
+      if (pos) {
+        sure = cross != 0;
+        const int at_lane = sure ? __ffs(cross) - 1 : 31 - __clz(pos);
+        int at = last;
+        if (sure) {
+#pragma unroll
+          for (int k = 7; k >= 0; --k)
+            if (w[k] > (k > 0 ? w[k > 0 ? k - 1 : 0] : 0.) && base + w[k] > c) at = k;
         }
-        token = i0 + l * 32 + __shfl_sync(kFull, at, l);
-      } else if (pos) {
-        const int l = 31 - __clz(pos);
-        fallback = i0 + l * 32 + __shfl_sync(kFull, lastpos, l);
+        token = lo + o + at_lane * 8 + __shfl_sync(kFull, at, at_lane);
       }
-      before += __shfl_sync(kFull, in, 31);
+      before += __shfl_sync(kFull, sum, 31);
     }
-    if (lane == 0) P.tokens[b * (P.K + 1) + n] = token >= 0 ? token : fallback;
+    if (lane == 0) P.tokens[b * (P.K + 1) + n] = token;
     return;
   }
 }
+
+constexpr int kMaxSampDevices = 64;
 
 bool al(const void* p, uintptr_t m) { return reinterpret_cast<uintptr_t>(p) % m == 0; }
 
 template <typename Args>
 rlk_status launch_clusters(void (*kern)(Args), const Args& a, int64_t groups, int C, int threads,
-                           cudaStream_t st) {
+                           cudaStream_t st, size_t smem = 0) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = dim3(static_cast<unsigned>(groups * C));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = st;
@@ -471,25 +735,38 @@ rlk_status launch_clusters(void (*kern)(Args), const Args& a, int64_t groups, in
   return RLK_OK;
 }
 
-template <typename TIn, typename TOut, int kThreads, int kN, int kBlocks, bool kResident>
-rlk_status launch_probs_as(ProbArgs a, int64_t R, int C, cudaStream_t st) {
-  a.slice = (a.V - 1) / C / 32 * 32 + 32;  // V / C rounded up to whole warps
-  return launch_clusters(probs_kernel<TIn, TOut, kThreads, kN, kBlocks, kResident>, a, R, C,
-                         kThreads, st);
+template <typename TIn, typename TOut, int kThreads>
+rlk_status launch_probs_as(const ProbArgs& a, int C, cudaStream_t st) {
+  static std::atomic<bool> raised[kMaxSampDevices];  // the kernel's shared-memory limit
+  int dev = 0;
+  auto kern = probs_kernel<TIn, TOut, kThreads>;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxSampDevices) {
+    cudaGetLastError();
+    return RLK_ERR_CUDA;
+  }
+  if (!raised[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kProbSlice + kProbPad)) != cudaSuccess) {
+      cudaGetLastError();
+      return RLK_ERR_CUDA;
+    }
+    raised[dev].store(true, std::memory_order_release);
+  }
+  return launch_clusters(kern, a, a.R, C, kThreads, st,
+                         static_cast<size_t>(a.slice) * sizeof(TIn) + kProbPad);
 }
 
-// The register plan of a V-entry row: 16 entries per thread on the smallest
-// cluster that holds it (several small CTAs share an SM, so that one's loads run
-// beside another's stores), more per thread where eight CTAs do not.
 template <typename TIn, typename TOut>
-rlk_status launch_probs(const ProbArgs& a, int64_t R, cudaStream_t st) {
-  const int V = a.V;
-  if (V <= 2048) return launch_probs_as<TIn, TOut, 256, 8, 4, true>(a, R, 1, st);
-  for (int C = 1; C <= kProbMaxCluster; C *= 2)
-    if (V <= C * 512 * 16) return launch_probs_as<TIn, TOut, 512, 16, 3, true>(a, R, C, st);
-  if (V <= 8 * 512 * 24) return launch_probs_as<TIn, TOut, 512, 24, 2, true>(a, R, 8, st);
-  if (V <= 8 * 512 * 40) return launch_probs_as<TIn, TOut, 512, 40, 2, true>(a, R, 8, st);
-  return launch_probs_as<TIn, TOut, 512, 16, 3, false>(a, R, 8, st);
+rlk_status launch_probs(ProbArgs a, cudaStream_t st) {
+  constexpr int kMost = static_cast<int>(kProbSlice / sizeof(TIn));
+  int C = 1;
+  while (C < kProbMaxCluster && a.V > C * kMost) C *= 2;
+  a.slice = (a.V - 1) / C / 32 * 32 + 32;  // V / C rounded up to whole warps
+  if (a.slice > kMost)
+    return launch_clusters(probs_long_kernel<TIn, TOut>, a, a.R, C, kProbLongThreads, st);
+  // short rows: small CTAs, more of them per SM
+  return a.V <= 2048 ? launch_probs_as<TIn, TOut, 128>(a, C, st)
+                     : launch_probs_as<TIn, TOut, kProbThreads>(a, C, st);
 }
 
 }  // namespace
@@ -529,15 +806,16 @@ extern "C" rlk_status rlk_token_probs(const void* logits, int logits_type, int64
   a.row_tau = row_temperature;
   a.ldx = ld_logits;
   a.ldp = ld_probs;
+  a.R = R;
   a.V = static_cast<int>(V);
   a.tau = temperature;
   a.err = static_cast<unsigned*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (logits_type == RLK_TYPE_F32)
-    return probs_type == RLK_TYPE_F32 ? launch_probs<float, float>(a, R, st)
-                                      : launch_probs<float, __nv_bfloat16>(a, R, st);
-  return probs_type == RLK_TYPE_F32 ? launch_probs<__nv_bfloat16, float>(a, R, st)
-                                    : launch_probs<__nv_bfloat16, __nv_bfloat16>(a, R, st);
+    return probs_type == RLK_TYPE_F32 ? launch_probs<float, float>(a, st)
+                                      : launch_probs<float, __nv_bfloat16>(a, st);
+  return probs_type == RLK_TYPE_F32 ? launch_probs<__nv_bfloat16, float>(a, st)
+                                    : launch_probs<__nv_bfloat16, __nv_bfloat16>(a, st);
 }
 
 extern "C" rlk_status rlk_draft_verify(const void* target_probs, int64_t target_stride_b,
@@ -580,12 +858,16 @@ extern "C" rlk_status rlk_draft_verify(const void* target_probs, int64_t target_
   a.us = u_sample;
   a.lens = draft_lens;
   a.K = K;
-  a.V = V;
+  a.V = static_cast<int>(V);
   a.tokens = tokens;
   a.accepted = num_accepted;
   a.err = static_cast<unsigned*>(workspace);
-  const int C = V <= 4096 ? 1 : V <= 16384 ? 2 : V <= 65536 ? 4 : 8;
-  a.seg = static_cast<int>((V - 1) / (C * kVerWarps) / 32 * 32 + 32);
+  a.seg = kVerPiece;
+  while ((V - 1) / a.seg >= kVerMaxSegs) a.seg *= 2;
+  a.nseg = static_cast<int>((V - 1) / a.seg + 1);
+  // as many CTAs as run at once (two per SM), each with a segment per warp at least
+  int C = 1;
+  while (C < kVerMaxCluster && B * C * 2 <= 2 * sms && a.nseg >= 2 * C * kVerWarps) C *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return probs_type == RLK_TYPE_F32
              ? launch_clusters(verify_kernel<float>, a, B, C, kVerThreads, st)
