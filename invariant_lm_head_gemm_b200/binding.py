@@ -6,7 +6,6 @@ is not a B200 the calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -573,16 +572,17 @@ def rlk_transition_logp(x, v, prev, a, c, s, want_mean=False, out=None, workspac
 _TYPE_IDS = {torch.bfloat16: 0, torch.float32: 1}  # RLK_TYPE_*
 
 
-def _scope(dev, stream):
-    """The context a call on tensors of `dev` runs in: that device is current,
-    and what the call allocates belongs to the stream it enqueues on."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
-        return torch.cuda.stream(stream)
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _on_stream(fn, dev, stream, *args):
+    """fn(*args, raw stream) with `dev` current, on `stream` (which then owns what
+    fn allocates) or on the device's current stream.  A rollout's calls take a few
+    microseconds on the GPU, so the usual case is kept short: no context, and the
+    stream's handle without its Python object."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if stream is not None and stream.device != dev:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+    with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 def _on(dev, t, dtypes, name, shape):
@@ -642,30 +642,31 @@ def rlk_token_probs(logits, temperature=1.0, dtype=None, out=None, workspace=Non
     fp32; the logits' own by default).  logits [..., V] bf16 or fp32, rows one
     stride apart; temperature a number or a CUDA fp32 tensor of the leading
     shape; 0 is greedy.  `out` may be the logits themselves."""
-    dev = logits.device
     ld = _row_stride(logits, "logits")
-    V = logits.shape[-1]
-    if V < 1:
+    if logits.shape[-1] < 1:
         raise ValueError("logits must have at least one entry per row")
-    R = logits.numel() // V
+    dev = logits.device
     row_t = None
     if isinstance(temperature, torch.Tensor):
         row_t, temperature = temperature, 1.0
         _on(dev, row_t, (torch.float32,), "temperature", tuple(logits.shape[:-1]))
-    with _scope(dev, stream):
-        if out is None:
-            out = torch.empty(logits.shape, dtype=dtype or logits.dtype, device=dev)
-            if out.dtype not in _TYPE_IDS:
-                raise ValueError("dtype must be bf16 or fp32")
-        elif out.device != dev or out.shape != logits.shape or (dtype and out.dtype != dtype):
-            raise ValueError("out must have the logits' shape and device, and the given dtype")
-        ld_out = _row_stride(out, "out")
-        workspace = sampling_workspace(dev) if workspace is None else _scratch(workspace, dev)
-        _check(_samp().rlk_token_probs(logits.data_ptr(), _TYPE_IDS[logits.dtype], R, V, ld,
-                                       float(temperature), _ptr(row_t), out.data_ptr(),
-                                       _TYPE_IDS[out.dtype], ld_out, workspace.data_ptr(),
-                                       workspace.numel(), _stream(stream)),
-               "rlk_token_probs")
+    if (dtype or logits.dtype) not in _TYPE_IDS:
+        raise ValueError("dtype must be bf16 or fp32")
+    if out is not None and (out.device != dev or out.shape != logits.shape or
+                            (dtype and out.dtype != dtype)):
+        raise ValueError("out must have the logits' shape and device, and the given dtype")
+    return _on_stream(_token_probs, dev, stream, logits, ld, temperature, row_t, dtype, out, workspace)
+
+
+def _token_probs(logits, ld, temperature, row_t, dtype, out, workspace, stream):
+    V = logits.shape[-1]
+    if out is None:
+        out = torch.empty_like(logits, dtype=dtype, memory_format=torch.contiguous_format)
+    ws = sampling_workspace(logits.device) if workspace is None else _scratch(workspace, logits.device)
+    _check(_samp().rlk_token_probs(
+        logits.data_ptr(), _TYPE_IDS[logits.dtype], logits.numel() // V, V, ld, temperature,
+        None if row_t is None else row_t.data_ptr(), out.data_ptr(), _TYPE_IDS[out.dtype],
+        _row_stride(out, "out"), ws.data_ptr(), ws.numel(), stream), "rlk_token_probs")
     return out
 
 
@@ -686,34 +687,35 @@ def rlk_draft_verify(target_probs, draft_probs, draft_tokens, u_accept, u_sample
         raise ValueError("target_probs must be [B, K+1, V] with V >= 1")
     if V > 1 and target_probs.stride(2) != 1:
         raise ValueError("target_probs must have contiguous rows")
-    q_sb = q_sk = 0
     if draft_probs is not None:
         if draft_probs.device != dev or draft_probs.dtype != target_probs.dtype or \
                 tuple(draft_probs.shape) != (B, K, V) or (V > 1 and draft_probs.stride(2) != 1):
             raise ValueError("draft_probs must be [B, K, V] of target_probs' type and device, "
                              "with contiguous rows")
-        q_sb, q_sk = draft_probs.stride(0), draft_probs.stride(1)
     _on(dev, draft_tokens, (torch.int64,), "draft_tokens", (B, K))
     _on(dev, u_accept, (torch.float32,), "u_accept", (B, K))
     _on(dev, u_sample, (torch.float32,), "u_sample", (B,))
     if draft_lens is not None:
         _on(dev, draft_lens, (torch.int64,), "draft_lens", (B,))
-    with _scope(dev, stream):
-        if out is None:
-            out = (torch.empty(B, K + 1, dtype=torch.int64, device=dev),
-                   torch.empty(B, dtype=torch.int64, device=dev))
-        else:
-            _on(dev, out[0], (torch.int64,), "tokens", (B, K + 1))
-            _on(dev, out[1], (torch.int64,), "num_accepted", (B,))
-        workspace = sampling_workspace(dev) if workspace is None else _scratch(workspace, dev)
-        _check(_samp().rlk_draft_verify(target_probs.data_ptr(), target_probs.stride(0),
-                                        target_probs.stride(1), _ptr(draft_probs), q_sb, q_sk,
-                                        _TYPE_IDS[target_probs.dtype], draft_tokens.data_ptr(),
-                                        u_accept.data_ptr(), u_sample.data_ptr(), _ptr(draft_lens),
-                                        B, K, V, out[0].data_ptr(), out[1].data_ptr(),
-                                        workspace.data_ptr(), workspace.numel(), _stream(stream)),
-               "rlk_draft_verify")
-    return out
+    if out is not None:
+        _on(dev, out[0], (torch.int64,), "tokens", (B, K + 1))
+        _on(dev, out[1], (torch.int64,), "num_accepted", (B,))
+    return _on_stream(_draft_verify, dev, stream, target_probs, draft_probs, draft_tokens, u_accept,
+                      u_sample, draft_lens, out, workspace)
+
+
+def _draft_verify(p, q, draft_tokens, u_accept, u_sample, draft_lens, out, workspace, stream):
+    B, K1, V = p.shape
+    tokens, accepted = out or (draft_tokens.new_empty((B, K1)), draft_tokens.new_empty(B))
+    ws = sampling_workspace(p.device) if workspace is None else _scratch(workspace, p.device)
+    p_sb, p_sk, _ = p.stride()
+    q_sb, q_sk, _ = (0, 0, 0) if q is None else q.stride()
+    _check(_samp().rlk_draft_verify(
+        p.data_ptr(), p_sb, p_sk, None if q is None else q.data_ptr(), q_sb, q_sk, _TYPE_IDS[p.dtype],
+        draft_tokens.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+        None if draft_lens is None else draft_lens.data_ptr(), B, K1 - 1, V, tokens.data_ptr(),
+        accepted.data_ptr(), ws.data_ptr(), ws.numel(), stream), "rlk_draft_verify")
+    return tokens, accepted
 
 
 _dis_fns = None
@@ -760,7 +762,7 @@ def _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse):
     _on(dev, teacher_logits, tuple(_TYPE_IDS), "teacher_logits", (T, K))
     if teacher_lse is not None:
         _on(dev, teacher_lse, (torch.float32,), "teacher_lse", (T,))
-    return dev, T, H, V, K
+    return dev, (T, H, V, K)
 
 
 def rlk_linear_distill_fwd(hidden, W, teacher_ids, teacher_logits, temperature=1.0,
@@ -771,23 +773,27 @@ def rlk_linear_distill_fwd(hidden, W, teacher_ids, teacher_logits, temperature=1
     slot), teacher_logits [T,K] fp32 or bf16, divided by teacher_temperature (the
     student's by default); teacher_lse [T] fp32 gives the teacher's own
     log-sum-exp instead of renormalising over the slots."""
-    dev, T, H, V, K = _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse)
+    dev, sizes = _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse)
+    if out is not None:
+        _on(dev, out[0], (torch.float32,), "loss", sizes[:1])
+        _on(dev, out[1], (torch.float32,), "lse", sizes[:1])
     if teacher_temperature is None:
         teacher_temperature = temperature
-    with _scope(dev, stream):
-        if workspace is None:
-            workspace = make_distill_workspace(T, H, V, K, False, dev)
-        _scratch(workspace, dev)
-        if out is None:
-            out = tuple(torch.empty(T, dtype=torch.float32, device=dev) for _ in range(2))
-        loss, lse = out
-        _on(dev, loss, (torch.float32,), "loss", (T,))
-        _on(dev, lse, (torch.float32,), "lse", (T,))
-        _check(_dis().rlk_linear_distill_fwd(
-            _ptr(hidden), _ptr(W), _ptr(teacher_ids), _ptr(teacher_logits),
-            _TYPE_IDS[teacher_logits.dtype], _ptr(teacher_lse), T, H, V, K, float(temperature),
-            float(teacher_temperature), _ptr(loss), _ptr(lse), _ptr(workspace), workspace.numel(),
-            _stream(stream)), "rlk_linear_distill_fwd")
+    return _on_stream(_distill_fwd, dev, stream, sizes, hidden, W, teacher_ids, teacher_logits,
+                      temperature, teacher_temperature, teacher_lse, workspace, out)
+
+
+def _distill_fwd(sizes, hidden, W, ids, logits, temperature, teacher_temperature, teacher_lse,
+                 workspace, out, stream):
+    dev = hidden.device
+    ws = make_distill_workspace(*sizes, False, dev) if workspace is None else _scratch(workspace, dev)
+    loss, lse = out or (hidden.new_empty(sizes[0], dtype=torch.float32),
+                        hidden.new_empty(sizes[0], dtype=torch.float32))
+    _check(_dis().rlk_linear_distill_fwd(
+        hidden.data_ptr(), W.data_ptr(), ids.data_ptr(), logits.data_ptr(), _TYPE_IDS[logits.dtype],
+        None if teacher_lse is None else teacher_lse.data_ptr(), *sizes, temperature,
+        teacher_temperature, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), stream),
+        "rlk_linear_distill_fwd")
     return loss, lse
 
 
@@ -796,32 +802,36 @@ def rlk_linear_distill_bwd(hidden, W, teacher_ids, teacher_logits, temperature, 
                            dW_dtype=torch.float32, stream=None):
     """(dHidden [T,H] bf16, dW [V,H]) for the loss gradients dloss [T] fp32 and the
     forward's lse; dW in dW_dtype (fp32 or bf16), or None for a frozen head."""
-    dev, T, H, V, K = _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse)
+    dev, sizes = _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse)
+    T, H, V, _ = sizes
     _on(dev, lse, (torch.float32,), "lse", (T,))
     _on(dev, dloss, (torch.float32,), "dloss", (T,))
     if dW_dtype is not None and dW_dtype not in _TYPE_IDS:
         raise ValueError("dW_dtype must be fp32, bf16 or None")
+    if out is not None:
+        _on(dev, out[0], (torch.bfloat16,), "dHidden", (T, H))
+        if (out[1] is None) != (dW_dtype is None):
+            raise ValueError("out must hold dW where dW_dtype is given, and only there")
+        if out[1] is not None:
+            _on(dev, out[1], (dW_dtype,), "dW", (V, H))
     if teacher_temperature is None:
         teacher_temperature = temperature
-    with _scope(dev, stream):
-        if workspace is None:
-            workspace = make_distill_workspace(T, H, V, K, True, dev)
-        _scratch(workspace, dev)
-        if out is None:
-            out = (torch.empty(T, H, dtype=torch.bfloat16, device=dev),
-                   None if dW_dtype is None else torch.empty(V, H, dtype=dW_dtype, device=dev))
-        dHidden, dW = out
-        _on(dev, dHidden, (torch.bfloat16,), "dHidden", (T, H))
-        if (dW is None) != (dW_dtype is None):
-            raise ValueError("out must hold dW where dW_dtype is given, and only there")
-        if dW is not None:
-            _on(dev, dW, (dW_dtype,), "dW", (V, H))
-        _check(_dis().rlk_linear_distill_bwd(
-            _ptr(hidden), _ptr(W), _ptr(teacher_ids), _ptr(teacher_logits),
-            _TYPE_IDS[teacher_logits.dtype], _ptr(teacher_lse), T, H, V, K, float(temperature),
-            float(teacher_temperature), _ptr(lse), _ptr(dloss), _ptr(dHidden), _ptr(dW),
-            _TYPE_IDS[dW_dtype or torch.float32], _ptr(workspace), workspace.numel(),
-            _stream(stream)), "rlk_linear_distill_bwd")
+    return _on_stream(_distill_bwd, dev, stream, sizes, hidden, W, teacher_ids, teacher_logits,
+                      temperature, teacher_temperature, teacher_lse, lse, dloss, workspace, out, dW_dtype)
+
+
+def _distill_bwd(sizes, hidden, W, ids, logits, temperature, teacher_temperature, teacher_lse, lse,
+                 dloss, workspace, out, dW_dtype, stream):
+    dev = hidden.device
+    ws = make_distill_workspace(*sizes, True, dev) if workspace is None else _scratch(workspace, dev)
+    dHidden, dW = out or (torch.empty_like(hidden),
+                          None if dW_dtype is None else torch.empty_like(W, dtype=dW_dtype))
+    _check(_dis().rlk_linear_distill_bwd(
+        hidden.data_ptr(), W.data_ptr(), ids.data_ptr(), logits.data_ptr(), _TYPE_IDS[logits.dtype],
+        None if teacher_lse is None else teacher_lse.data_ptr(), *sizes, temperature,
+        teacher_temperature, lse.data_ptr(), dloss.data_ptr(), dHidden.data_ptr(),
+        None if dW is None else dW.data_ptr(), _TYPE_IDS[dW_dtype or torch.float32], ws.data_ptr(),
+        ws.numel(), stream), "rlk_linear_distill_bwd")
     return dHidden, dW
 
 
