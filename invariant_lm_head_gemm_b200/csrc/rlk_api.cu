@@ -224,13 +224,22 @@ rlk_status write_chunk_words(uint32_t* words, int64_t n, uint32_t seq, cudaStrea
 
 std::atomic<int> g_max_clusters[kModes][kMaxDevices];
 
+// Lets a kernel start before the one ahead of it in the stream has ended (it
+// waits for that one's results itself: grid_dependency_wait).
+cudaLaunchAttribute programmatic_launch() {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
 // Launches pair_kernel<Mode> on clusters of two CTAs: at most one cluster per
 // unit and no more clusters than can be resident at once.  `cooperative`
 // makes the launch fail rather than start with some CTAs not resident (the
 // backward's units wait on each other).
 template <int Mode>
 rlk_status launch_pair(const typename ModeArgs<Mode>::type& args, long long total,
-                       bool cooperative, cudaStream_t st) {
+                       bool cooperative, cudaStream_t st, bool after_prep = false) {
   if (total <= 0) return RLK_OK;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -247,7 +256,7 @@ rlk_status launch_pair(const typename ModeArgs<Mode>::type& args, long long tota
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = PipeCfg<Mode>::kSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -268,6 +277,7 @@ rlk_status launch_pair(const typename ModeArgs<Mode>::type& args, long long tota
     g_max_clusters[Mode][dev].store(n, std::memory_order_relaxed);
   }
   cfg.numAttrs = cooperative ? 2 : 1;
+  if (after_prep) attr[cfg.numAttrs++] = programmatic_launch();
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(total, mc)));
   if (cudaLaunchKernelEx(&cfg, kern, args) != cudaSuccess) {
     cudaGetLastError();
@@ -322,7 +332,7 @@ rlk_status launch_short(DecArgs& a, bool store, cudaStream_t st, bool half = fal
   cfg.blockDim = dim3(kDecThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kDecCluster;
   attr[0].val.clusterDim.y = 1;
@@ -341,6 +351,7 @@ rlk_status launch_short(DecArgs& a, bool store, cudaStream_t st, bool half = fal
     mc = n;
     cache.store(n, std::memory_order_relaxed);
   }
+  if (distill) attr[cfg.numAttrs++] = programmatic_launch();
   cfg.gridDim = dim3(static_cast<unsigned>(kDecCluster * std::min<int>(a.NG, mc)));
   if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
     cudaGetLastError();
@@ -413,7 +424,7 @@ rlk_status enqueue_fwd_partials(const rlk_bf16* hidden, const rlk_bf16* W, const
   a.KB = static_cast<int>(H / kBK);
   a.total = static_cast<long long>(a.MT) * a.NG;
   a.ep.dis = dis ? *dis : DistillRows{};
-  return dis ? launch_pair<kModeFwdDistill>(a, a.total, false, st)
+  return dis ? launch_pair<kModeFwdDistill>(a, a.total, false, st, true)
              : launch_pair<kModeFwd>(a, a.total, false, st);
 }
 
@@ -520,11 +531,14 @@ rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
   P.dloss = dloss;
   P.dw_bf16 = dw_bf16 ? 1 : 0;
 
-  if (cudaMemsetAsync(cnt, 0, bwd_counter_words(pl) * 4, st) != cudaSuccess) return RLK_ERR_CUDA;
+  // (the distillation's counters are cleared before its preparation, behind which
+  // this launch does not wait)
+  if (!dis && cudaMemsetAsync(cnt, 0, bwd_counter_words(pl) * 4, st) != cudaSuccess)
+    return RLK_ERR_CUDA;
   // Units wait on units claimed earlier, and only running CTA pairs claim
   // units, so no pair ever waits on one that has not started: the launch needs
   // no co-residency guarantee.
-  return dis ? launch_pair<kModeBwdDistill>(P, pl.total, false, st)
+  return dis ? launch_pair<kModeBwdDistill>(P, pl.total, false, st, true)
              : launch_pair<kModeBwd>(P, pl.total, false, st);
 }
 
@@ -1208,7 +1222,7 @@ namespace {
 
 // The sorted slots and their table behind a pass's own scratch, from `base`.
 struct DistillLayout {
-  size_t ids, logq, y, sum, count, first, end;
+  size_t ids, logq, y, sum, count, head, end;
   int64_t G;
 };
 
@@ -1221,8 +1235,8 @@ DistillLayout distill_layout(size_t base, int64_t T, int64_t V, int64_t K, int s
   L.y = L.logq + align256(t * k * 4);
   L.sum = L.y + align256(t * k * 4);
   L.count = L.sum + align256(t * 4);
-  L.first = L.count + align256(t * 4);
-  L.end = L.first + align256(t * static_cast<size_t>(L.G + 1) * 2);
+  L.head = L.count + align256(t * 4);
+  L.end = L.head + align256(t * static_cast<size_t>(L.G) * sizeof(uint2));
   return L;
 }
 
@@ -1233,9 +1247,9 @@ DistillRows distill_rows(uint8_t* ws, const DistillLayout& L, int64_t K) {
   D.y = reinterpret_cast<float*>(ws + L.y);
   D.sum = reinterpret_cast<float*>(ws + L.sum);
   D.count = reinterpret_cast<int*>(ws + L.count);
-  D.first = reinterpret_cast<uint16_t*>(ws + L.first);
+  D.head = reinterpret_cast<uint2*>(ws + L.head);
   D.ld = static_cast<int>(K);
-  D.entries = static_cast<int>(L.G + 1);
+  D.G = static_cast<int>(L.G);
   return D;
 }
 
@@ -1251,18 +1265,17 @@ rlk_status check_distill(int64_t T, int64_t H, int64_t V, int64_t K, float tempe
 
 rlk_status enqueue_distill_prep(const int64_t* ids, const void* logits, int logits_type,
                                 const float* teacher_lse, int64_t T, int64_t V, int64_t K,
-                                float teacher_temperature, int64_t G, int shift,
-                                const DistillRows& D, cudaStream_t st) {
+                                float teacher_temperature, int shift, const DistillRows& D,
+                                cudaStream_t st) {
   const unsigned blocks = static_cast<unsigned>(ceil_div(T, 4));
-  const int t = static_cast<int>(T), k = static_cast<int>(K), v = static_cast<int>(V),
-            g = static_cast<int>(G);
+  const int t = static_cast<int>(T), k = static_cast<int>(K), v = static_cast<int>(V);
   if (logits_type == RLK_TYPE_F32) {
     distill_prep_kernel<float><<<blocks, 128, 0, st>>>(ids, static_cast<const float*>(logits),
-                                                       teacher_lse, t, k, v, g, shift,
+                                                       teacher_lse, t, k, v, shift,
                                                        teacher_temperature, D);
   } else {
     distill_prep_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(
-        ids, static_cast<const __nv_bfloat16*>(logits), teacher_lse, t, k, v, g, shift,
+        ids, static_cast<const __nv_bfloat16*>(logits), teacher_lse, t, k, v, shift,
         teacher_temperature, D);
   }
   return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
@@ -1310,15 +1323,26 @@ rlk_status rlk_linear_distill_fwd(const rlk_bf16* hidden, const rlk_bf16* W,
   float* pb = reinterpret_cast<float*>(ws + L.pb);
   const DistillRows D = distill_rows(ws, DL, K);
   if ((s = enqueue_distill_prep(teacher_ids, teacher_logits, logits_type, teacher_lse, T, V, K,
-                                teacher_temperature, DL.G, kDisFwdShift, D, st)) != RLK_OK)
+                                teacher_temperature, kDisFwdShift, D, st)) != RLK_OK)
     return s;
   if ((s = enqueue_fwd_partials(hidden, W, nullptr, T, H, V, 0, temperature, pm, ps, pb,
                                 fwd_groups(V), reinterpret_cast<float*>(ws + L.yt), err, st,
                                 &D)) != RLK_OK)
     return s;
-  distill_combine_kernel<<<static_cast<unsigned>(ceil_div(T, 8)), 256, 0, st>>>(
-      pm, ps, pb, D, static_cast<int>(T), static_cast<int>(fwd_groups(V)), loss, lse, err);
-  return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(T, 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = programmatic_launch();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const float *m = pm, *sum = ps, *b = pb;
+  if (cudaLaunchKernelEx(&cfg, distill_combine_kernel, m, sum, b, D, static_cast<int>(T),
+                         static_cast<int>(fwd_groups(V)), loss, lse, err) != cudaSuccess) {
+    cudaGetLastError();
+    return RLK_ERR_CUDA;
+  }
+  return RLK_OK;
 }
 
 rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
@@ -1352,8 +1376,11 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
   if ((s = check_device(&sms)) != RLK_OK) return s;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const DistillRows D = distill_rows(ws, DL, K);
+  const BwdPlan pl = make_bwd_plan(T, H, V, vchunk(V), dW != nullptr);
+  if (cudaMemsetAsync(ws + L.cnt, 0, bwd_counter_words(pl) * 4, st) != cudaSuccess)
+    return RLK_ERR_CUDA;
   if ((s = enqueue_distill_prep(teacher_ids, teacher_logits, logits_type, teacher_lse, T, V, K,
-                                teacher_temperature, DL.G, kDisBwdShift, D, st)) != RLK_OK)
+                                teacher_temperature, kDisBwdShift, D, st)) != RLK_OK)
     return s;
   return enqueue_bwd(hidden, W, nullptr, T, H, V, 0, V, temperature, lse, nullptr, nullptr, nullptr,
                      dHidden, nullptr, 0, 0, static_cast<float*>(dW), ws, L, st, kWaitLimitNs, 0,

@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
     // q+1 (or, for q = 3, to CTA rank+1 / the split's partial), so every row
     // still folds its chunks in ascending column order while the four warps
     // (and the four CTAs) work on different blocks at once.
+    if constexpr (kDistill) grid_dependency_wait();  // the teacher's rows
     const int q = warp & 3;
     float* xt = XT + q * 32 * kDecXStride;
     const int nblk = (N + 31) / 32;
@@ -459,9 +460,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
           // the four transposition tiles.
           const int t = lane;
           int64_t tgt = -1;
-          int f0 = 0, f1 = 0;  // distillation: the row's slots in this split
+          DisCursor slots;  // distillation: the row's slots in this split
           if constexpr (kDistill) {
-            if (t < P.ep.T) dis_range(P.ep.dis, t, static_cast<int>(u), f0, f1);
+            slots.none();
+            if (t < P.ep.T) slots.begin(P.ep.dis, t, static_cast<int>(u));
           } else {
             if (t < P.ep.T) tgt = P.ep.targets[t] - P.ep.v0;
           }
@@ -512,8 +514,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
               y[4 * i + 2] = fwd_scale(f.z, P.ep.scale_log2);
               y[4 * i + 3] = fwd_scale(f.w, P.ep.scale_log2);
             }
-            if constexpr (kDistill)
-              dis_capture(P.ep.dis, static_cast<size_t>(t) * P.ep.dis.ld, y, tile0 + c * 32, f0, f1);
+            if constexpr (kDistill) dis_capture(P.ep.dis, slots, y, tile0 + c * 32);
             if (t < P.ep.T) fwd_chunk_update(y, tile0 + c * 32, P.ep.V, tgt, P.ep.ytgt + t, m, s, b);
           }
           mbar_arrive(xfree_bar);
@@ -535,9 +536,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
         for (int blk = 0; blk < nblk; ++blk, ++g) {
           const int t = blk * 32 + lane;
           int64_t tgt = -1;  // loaded early, as the range is
-          int f0 = 0, f1 = 0;
+          DisCursor slots;
           if constexpr (kDistill) {
-            if (t < P.ep.T) dis_range(P.ep.dis, t, static_cast<int>(u), f0, f1);
+            slots.none();
+            if (t < P.ep.T) slots.begin(P.ep.dis, t, static_cast<int>(u));
           } else {
             if (t < P.ep.T) tgt = P.ep.targets[t] - P.ep.v0;
           }
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_fwd_kernel(const __grid
           for (int i = 0; i < 32; ++i) y[i] = fwd_scale(xt[i * kDecXStride + lane], P.ep.scale_log2);
           __syncwarp();  // the tile is free for the next block
           if constexpr (kDistill) {  // before the wait below: not part of the chain
-            dis_capture(P.ep.dis, static_cast<size_t>(t) * P.ep.dis.ld, y, col0, f0, f1);
+            dis_capture(P.ep.dis, slots, y, col0);
             __syncwarp();
           }
           // 2. the rows' running triples

@@ -22,19 +22,21 @@
 namespace rlk {
 
 // One warp per row: the used slots sorted by (id, slot), their log weights, the
-// number of slots with ids below every 2^shift columns, Q and the count.  A rank
+// table of where every 2^shift columns' slots begin, Q and the count.  A rank
 // sort: at most K^2 / 32 comparisons per lane, from shared memory, beside the
 // T x H x V product it prepares.  Sums run over the sorted slots, so a row's
-// results do not depend on the order in which its slots are given.
+// results do not depend on the order in which its slots are given.  The kernel
+// that reads all this is let in at once: only its epilogue has to wait.
 template <typename TLogit>
 __global__ void __launch_bounds__(128) distill_prep_kernel(
     const int64_t* __restrict__ ids, const TLogit* __restrict__ logits,
-    const float* __restrict__ teacher_lse, int T, int K, int V, int G, int shift, float tau,
+    const float* __restrict__ teacher_lse, int T, int K, int V, int shift, float tau,
     const DistillRows D) {
   __shared__ int key[4][kDisMaxK];
   __shared__ float val[4][kDisMaxK];
   __shared__ int skey[4][kDisMaxK];
   __shared__ float sval[4][kDisMaxK];
+  grid_dependents_go();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * 4 + w;
   if (t >= T) return;  // warp-uniform; only warp-level synchronisation below
@@ -108,18 +110,22 @@ __global__ void __launch_bounds__(128) distill_prep_kernel(
     D.sum[t] = Q;
     D.count[t] = n | (bad ? kDisBad : 0);
   }
-  for (int g = lane; g <= G; g += 32) {
-    const int64_t c = static_cast<int64_t>(g) << shift;
-    int lo = 0, hi = n;  // the first slot with an id of at least c
+  uint2* head = D.head + static_cast<size_t>(t) * D.G;
+  for (int g = lane; g < D.G; g += 32) head[g] = make_uint2(kDisEnd, 0u);
+  __syncwarp();  // the columns that have slots are written after all are cleared
+  for (int i = lane; i < n; i += 32) {
+    const int g = skey[w][i] >> shift;
+    if (i > 0 && skey[w][i - 1] >> shift == g) continue;
+    int lo = i + 1, hi = n;  // the first slot of a later column
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (skey[w][mid] < c) {
+      if (skey[w][mid] >> shift == g) {
         lo = mid + 1;
       } else {
         hi = mid;
       }
     }
-    D.first[static_cast<size_t>(t) * (G + 1) + g] = static_cast<uint16_t>(lo);
+    head[g] = make_uint2(static_cast<uint32_t>(skey[w][i]), static_cast<uint32_t>(i | lo << 16));
   }
 }
 
@@ -129,6 +135,7 @@ __global__ void __launch_bounds__(256) distill_combine_kernel(
     const float* __restrict__ pm, const float* __restrict__ ps, const float* __restrict__ pb,
     const DistillRows D, int T, int G, float* __restrict__ loss, float* __restrict__ lse,
     uint32_t* err) {
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= T) return;  // warp-uniform
@@ -170,7 +177,6 @@ struct EpiDistill {
   };
   struct State {
     float A, coef, all;  // all = coef Q
-    size_t row0;
     int row;
     bool valid;
   };
@@ -179,12 +185,10 @@ struct EpiDistill {
     st.row = row;
     st.valid = row < p.T;
     st.A = st.coef = st.all = 0.f;
-    st.row0 = 0;
     if (st.valid) {
       st.A = p.lse[row] * kLog2e;
       st.coef = p.inv_tau * p.dloss[row];
       st.all = st.coef * p.D.sum[row];
-      st.row0 = static_cast<size_t>(row) * p.D.ld;
     }
   }
 
@@ -192,10 +196,12 @@ struct EpiDistill {
                               const CUtensorMap* store_map, uint32_t stage, int lane,
                               int warp_row0) {
     const bool any_row = warp_row0 < p.T;
-    int cur = 0, end = 0, nxt = kDisEnd;
+    DisCursor slots;
+    slots.none();
+    float logq = 0.f;  // of the cursor's slot, loaded ahead like its id
     if (st.valid) {
-      dis_range(p.D, st.row, (p.c0 + nt * kBN) >> kDisBwdShift, cur, end);
-      if (cur < end) nxt = p.D.ids[st.row0 + cur];
+      slots.begin(p.D, st.row, (p.c0 + nt * kBN) >> kDisBwdShift);
+      if (slots.cur < slots.end) logq = p.D.logq[slots.row0 + slots.cur];
     }
 #pragma unroll 1
     for (int c = 0; c < kBN / 32; ++c) {
@@ -212,13 +218,13 @@ struct EpiDistill {
         for (int j = 0; j < 32; ++j)
           if (col0 + j >= p.V) dx[j] = 0.f;
       }
-      while (nxt < col0 + 32) {
-        const int d = nxt - col0;
-        const float hit = st.coef * dis_weight(p.D.logq[st.row0 + cur]);
+      while (slots.nxt < col0 + 32) {
+        const int d = slots.nxt - col0;
+        const float hit = st.coef * dis_weight(logq);
+        slots.next(p.D);
+        if (slots.cur < slots.end) logq = p.D.logq[slots.row0 + slots.cur];
 #pragma unroll
         for (int j = 0; j < 32; ++j) dx[j] = (j == d) ? dx[j] - hit : dx[j];
-        ++cur;
-        nxt = cur < end ? p.D.ids[st.row0 + cur] : kDisEnd;
       }
       __syncwarp();
       if (any_row) store_dx_chunk(dx, store_map, stage + (c & 1) * 2048u, lane, loc0, warp_row0);

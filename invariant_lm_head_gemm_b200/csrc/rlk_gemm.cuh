@@ -32,60 +32,67 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // A teacher's top logits for the distillation kernels (rlk_distill.cuh): per row,
-// the used slots sorted by vocab id, and how many lie below each table column.
+// the used slots sorted by vocab id, and for every 2^shift columns where they begin.
 struct DistillRows {
   int* ids;          // [T][ld] sorted ids
   float* logq;       // [T][ld] log weights
   float* y;          // [T][ld] the student's scaled logits there (forward)
   float* sum;        // [T] sum of the weights
   int* count;        // [T] used slots, and a flag
-  uint16_t* first;   // [T][entries] slots with ids below (column << shift)
+  uint2* head;       // [T][G] a table column's first id (kDisEnd: none), its slots' begin | end << 16
   int ld;            // slots per row
-  int entries;       // table entries per row
+  int G;             // table columns
 };
 
 constexpr int kDisMaxK = 256;
 constexpr int kDisEnd = 0x7fffffff;  // past every vocab id
 constexpr int kDisBad = 1 << 30;     // flag beside a row's count: an id outside [0, V)
-constexpr int kDisFwdShift = 9;      // columns per table entry: a forward split (512) ...
-constexpr int kDisBwdShift = 8;      // ... and a recompute tile (256)
+constexpr int kDisFwdShift = 9;      // a table column of the forward: its split (512) ...
+constexpr int kDisBwdShift = 8;      // ... and of the backward: its recompute tile (256)
 
 // The weight of a slot from its stored logarithm.
 __device__ __forceinline__ float dis_weight(float logq) { return expf(logq); }
 
-// Picks y[d] of a register array.
-__device__ __forceinline__ float dis_select(const float (&y)[32], int d) {
-  float v = y[0];
-#pragma unroll
-  for (int j = 1; j < 32; ++j) v = (j == d) ? y[j] : v;
-  return v;
-}
-
-// The logits y at this row's ids within columns col0 .. col0 + 31, for a walk in
-// ascending columns: `cur` is the next sorted slot, `nxt` its id.
-__device__ __forceinline__ void dis_capture_next(const DistillRows& D, size_t row0,
-                                                 const float (&y)[32], int col0, int& cur, int end,
-                                                 int& nxt) {
-  while (nxt < col0 + 32) {
-    D.y[row0 + cur] = dis_select(y, nxt - col0);
-    ++cur;
-    nxt = cur < end ? D.ids[row0 + cur] : kDisEnd;
+// The slots of one row within one table column, walked in ascending columns.  The
+// table gives the first id, so a column with one slot (nearly all that have any)
+// costs one load; the id after the next is loaded when the next comes into use, so
+// a hit waits for no load either.
+struct DisCursor {
+  size_t row0;
+  int cur, end;
+  int nxt, after;  // the ids of slots cur and cur + 1
+  __device__ __forceinline__ void none() {
+    row0 = 0;
+    cur = end = 0;
+    nxt = after = kDisEnd;
   }
-}
+  __device__ __forceinline__ void begin(const DistillRows& D, int row, int g) {
+    const uint2 h = D.head[static_cast<size_t>(row) * D.G + g];
+    row0 = static_cast<size_t>(row) * D.ld;
+    nxt = static_cast<int>(h.x);
+    cur = static_cast<int>(h.y & 0xffffu);
+    end = static_cast<int>(h.y >> 16);
+    after = cur + 1 < end ? D.ids[row0 + cur + 1] : kDisEnd;
+  }
+  __device__ __forceinline__ void next(const DistillRows& D) {
+    ++cur;
+    nxt = after;
+    after = cur + 1 < end ? D.ids[row0 + cur + 1] : kDisEnd;
+  }
+};
 
-// The slots of row `row` in table column g.
-__device__ __forceinline__ void dis_range(const DistillRows& D, int row, int g, int& f0, int& f1) {
-  const uint16_t* f = D.first + static_cast<size_t>(row) * D.entries + g;
-  f0 = f[0];
-  f1 = f[1];
-}
-
-// The same for a chunk met on its own, among the slots [f0, f1) of its split.
-__device__ __forceinline__ void dis_capture(const DistillRows& D, size_t row0,
-                                            const float (&y)[32], int col0, int f0, int f1) {
-  for (int i = f0; i < f1; ++i) {
-    const int d = D.ids[row0 + i] - col0;
-    if (d >= 0 && d < 32) D.y[row0 + i] = dis_select(y, d);
+// Stores the logits y at this row's ids within columns col0 .. col0 + 31.
+__device__ __forceinline__ void dis_capture(const DistillRows& D, DisCursor& c,
+                                            const float (&y)[32], int col0) {
+  while (c.nxt < col0 + 32) {
+    const int d = c.nxt - col0;
+    if (d >= 0) {  // a chunk met on its own skips the slots before it
+      float v = y[0];
+#pragma unroll
+      for (int j = 1; j < 32; ++j) v = (j == d) ? y[j] : v;
+      D.y[c.row0 + c.cur] = v;
+    }
+    c.next(D);
   }
 }
 
@@ -164,7 +171,7 @@ struct EpiFwd {
     int64_t tgt;
     int row;
     bool valid;
-    int cur, end, nxt;  // distillation: the slots of this split still to come
+    DisCursor cursor;  // distillation: the slots of this split still to come
   };
 
   template <bool kDistill>
@@ -173,12 +180,8 @@ struct EpiFwd {
     st.valid = row < p.T;
     if constexpr (kDistill) {
       st.tgt = -1;
-      st.cur = st.end = 0;
-      st.nxt = kDisEnd;
-      if (st.valid) {
-        dis_range(p.dis, row, g, st.cur, st.end);
-        if (st.cur < st.end) st.nxt = p.dis.ids[static_cast<size_t>(row) * p.dis.ld + st.cur];
-      }
+      st.cursor.none();
+      if (st.valid) st.cursor.begin(p.dis, row, g);
     } else {
       st.tgt = st.valid ? p.targets[row] - p.v0 : -1;  // local column of the target
     }
@@ -197,8 +200,7 @@ struct EpiFwd {
 #pragma unroll
       for (int j = 0; j < 32; ++j) y[j] = fwd_scale(__uint_as_float(r[j]), p.scale_log2);
       if constexpr (kDistill) {
-        dis_capture_next(p.dis, static_cast<size_t>(st.row) * p.dis.ld, y, nt * kBN + c * 32, st.cur,
-                         st.end, st.nxt);
+        dis_capture(p.dis, st.cursor, y, nt * kBN + c * 32);
         __syncwarp();
       }
       fwd_chunk_update(y, nt * kBN + c * 32, p.V, st.tgt, p.ytgt + st.row, st.m, st.s, st.b);

@@ -548,6 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
+    constexpr bool kDistill = Mode == kModeFwdDistill || Mode == kModeBwdDistill;
+    if constexpr (kDistill) grid_dependency_wait();  // the teacher's rows
     const int q = warp & 3;
     const int row_in_tile = q * 32 + lane;
     const int row_off = kBM * static_cast<int>(rank) + row_in_tile;
@@ -567,7 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Job j = make_job(P, u);
       if (j.type < 0) break;
       typename EpiFwd::State fst;
-      constexpr bool kDistill = Mode == kModeFwdDistill || Mode == kModeBwdDistill;
       if constexpr (is_fwd(Mode))
         EpiFwd::begin_unit<kDistill>(P.ep, fst, j.mt * kPairM + row_off, j.nt / P.group);
       for (int t = 0; t < j.ntiles; ++t, ++tc) {

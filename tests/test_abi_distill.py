@@ -67,8 +67,8 @@ def test_workspace_bytes(L):
     def a(x):
         return (x + 255) // 256 * 256
     rows = 3 * a(T * K * 4) + 2 * a(T * 4)
-    assert f(T, H, V, K, 0) == binding.workspace_bytes(T, H, V, False) + rows + a(T * 298 * 2)
-    assert f(T, H, V, K, 1) == binding.workspace_bytes(T, H, V, True) + rows + a(T * 595 * 2)
+    assert f(T, H, V, K, 0) == binding.workspace_bytes(T, H, V, False) + rows + a(T * 297 * 8)
+    assert f(T, H, V, K, 1) == binding.workspace_bytes(T, H, V, True) + rows + a(T * 594 * 8)
     assert f(1, 64, 1, 1, 1) >= f(1, 64, 1, 1, 0) > 256
 
 
