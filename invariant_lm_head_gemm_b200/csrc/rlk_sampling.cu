@@ -15,6 +15,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -471,7 +472,8 @@ __global__ void __launch_bounds__(kProbLongThreads) probs_long_kernel(const Prob
 // cluster's size, which follows the number of sequences.
 //
 // Bound by latency at few sequences (the drafts, their entries, the row, the
-// walk: four round trips and a cluster barrier) and by HBM at many.
+// walk: four round trips and a cluster barrier), by instructions and then by HBM at
+// many.
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerMaxCluster = 8;
@@ -499,19 +501,107 @@ struct VerifyArgs {
 // x 2^-896 in 64 bits, exactly: the exponent's field moved, not rebiased (a shift
 // and a mask, where converting takes the slow path of the conversion unit; zeros
 // and subnormals come out right by themselves).  Sums of such values, and their
-// comparison with a share of their own sum, need no scaling back.  An infinite x
-// becomes 2^-768, which kVerHuge tells from a sum of probabilities.
+// comparison with a share of their own sum, need no scaling back.
+template <typename T>
 __device__ __forceinline__ double scaled(float x) {
   const int u = __float_as_int(x);
-  return __hiloint2double((u >> 3) & static_cast<int>(0x8fffffffu), u << 29);
+  // a bf16 has no bits that reach the lower word
+  return __hiloint2double((u >> 3) & static_cast<int>(0x8fffffffu), sizeof(T) == 2 ? 0 : u << 29);
 }
-constexpr double kVerHuge = 0x1p-769;
 
-// max(0, p - q), scaled; `bad` where it is NaN.
-__device__ __forceinline__ double residual(float p, float q, bool& bad) {
-  const float d = p - q;  // of the exact difference's sign
-  bad |= d != d;
-  return d > 0.f ? scaled(p) - scaled(q) : 0.;
+// max(0, p - q), scaled; `odd` becomes NaN where either is NaN or infinite.
+template <typename T>
+__device__ __forceinline__ double residual(float p, float q, float& odd) {
+  odd = fmaf(p, 0.f, fmaf(q, 0.f, odd));
+  return scaled<T>(fmaxf(p, q)) - scaled<T>(q);
+}
+
+// The index in a 256-entry piece of a lane's entry j: one by one in fp32, pairs of
+// neighbours in bf16.
+template <typename T>
+__device__ __forceinline__ int piece_index(int lane, int j) {
+  return sizeof(T) == 4 ? lane + 32 * j : 2 * lane + 64 * (j >> 1) + (j & 1);
+}
+
+// A lane's 8 entries of the piece at `row`, all of it inside the row.  kOdd: a bf16
+// piece that starts off a word's boundary; each pair is put together from two lanes'
+// words, and nothing outside the piece but the entry before it, in the same word,
+// is read (`begins`: not even that, the row begins here).
+template <bool kOdd>
+__device__ __forceinline__ void load_piece(float (&v)[8], const float* row, bool, int lane) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = row[lane + 32 * j];
+}
+template <bool kOdd>
+__device__ __forceinline__ void load_piece(float (&v)[8], const __nv_bfloat16* row, bool begins,
+                                           int lane) {
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(row);
+  const uint32_t* x = reinterpret_cast<const uint32_t*>(h - (kOdd ? 1 : 0)) + lane;
+  uint32_t w[4], behind = 0u;
+  if constexpr (kOdd) {
+    const bool lone = begins && lane == 0;
+    w[0] = lone ? static_cast<uint32_t>(h[0]) << 16 : x[0];
+    if (lane == 0) behind = h[kVerPiece - 1];
+  } else {
+    w[0] = x[0];
+  }
+#pragma unroll
+  for (int j = 1; j < 4; ++j) w[j] = x[32 * j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t two = w[j];
+    if constexpr (kOdd) {  // lane 31 goes on in lane 0's next word
+      const uint32_t give = lane == 0 ? (j < 3 ? w[j < 3 ? j + 1 : 3] : behind) : w[j];
+      two = __funnelshift_r(two, __shfl_sync(kFull, give, (lane + 1) & 31), 16);
+    }
+    v[2 * j] = __uint_as_float(two << 16);
+    v[2 * j + 1] = __uint_as_float(two & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ double tree8(const double (&r)[8]) {
+  return ((r[0] + r[1]) + (r[2] + r[3])) + ((r[4] + r[5]) + (r[6] + r[7]));
+}
+
+// A lane's part of the residual's sum over one whole segment; kQ: there is a q.
+// The alignment and q are the row's: the loop over segments is compiled for each
+// kind, with no condition left inside (as conditions they took 40 instructions
+// per entry instead of 15).
+template <typename T, bool kQ, bool kOddP, bool kOddQ>
+__device__ __forceinline__ double segment_part(const T* p, const T* q, int lo, int seg, int lane,
+                                               float& odd) {
+  double acc = 0.;
+  for (int o = lo; o < lo + seg; o += kVerPiece) {
+    float pv[8], qv[8];
+    load_piece<kOddP>(pv, p + o, o == 0, lane);
+    if constexpr (kQ) load_piece<kOddQ>(qv, q + o, o == 0, lane);
+    double r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = residual<T>(pv[j], kQ ? qv[j] : 0.f, odd);
+    acc += tree8(r);
+  }
+  return acc;
+}
+
+// The same for any segment: cut off by the row's end, or with the place where q is
+// one in it.
+template <typename T>
+__device__ __forceinline__ double any_segment_part(const T* p, const T* q, int hot, int V, int lo,
+                                                   int seg, int lane, float& odd) {
+  double acc = 0.;
+  for (int o = 0; o < seg; o += kVerPiece) {
+    double r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = o + piece_index<T>(lane, j);
+      const bool in = at < V - lo;
+      const float pv = in ? to_f32(p[lo + at]) : 0.f;
+      const float qv = in && q ? to_f32(q[lo + at]) : in && lo + at == hot ? 1.f : 0.f;
+      r[j] = residual<T>(pv, qv, odd);
+    }
+    acc += tree8(r);
+  }
+  return acc;
 }
 
 template <typename T>
@@ -573,37 +663,39 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel
   const int my = static_cast<int>(rank) * kVerWarps + warp;  // segments my, my + nw, ...
 
   for (int attempt = 0;; ++attempt) {
-    // the residual of 8 entries, i + step j, as far as `left` goes
-    bool bad = false;
-    auto add8 = [&](double acc, int i, int left) {
-      float pv[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) pv[j] = lane < left - 32 * j ? to_f32(p[i + 32 * j]) : 0.f;
-      if (q) {
-        float qv[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) qv[j] = lane < left - 32 * j ? to_f32(q[i + 32 * j]) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc += residual(pv[j], qv[j], bad);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc += residual(pv[j], i + 32 * j == hot ? 1.f : 0.f, bad);
-      }
-      return acc;
-    };
+    float odd = 0.f;
     if (attempt == 0) cluster_all_started();
-    for (int s = my; s < P.nseg; s += nw) {
-      const int lo = s * P.seg, size = min(P.seg, V - lo);
-      double acc = 0.;
-      for (int o = 0; o < size; o += kVerPiece) acc = add8(acc, lo + o + lane, size - o);
+    auto put = [&](int s, double acc) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
-      if (__any_sync(kFull, bad)) acc = static_cast<double>(NAN);
+      if (__any_sync(kFull, odd != 0.f)) acc = static_cast<double>(NAN);  // no distribution
       if (lane < C)
         st_cluster_v2(mapa_shared(smem_u32(&totals[attempt][s]), lane),
                       static_cast<uint32_t>(__double2loint(acc)),
                       static_cast<uint32_t>(__double2hiint(acc)));
+    };
+    const int whole = V / P.seg;
+    const int hot_seg = hot >= 0 ? hot / P.seg : -1;
+    auto sums = [&](auto kq, auto kp, auto kr) {
+      for (int s = my; s < whole; s += nw) {
+        put(s, kq.value || s != hot_seg
+                   ? segment_part<T, kq.value, kp.value, kr.value>(p, q, s * P.seg, P.seg, lane, odd)
+                   : any_segment_part(p, q, hot, V, s * P.seg, P.seg, lane, odd));
+      }
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    const bool odd_p = sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(p) & 2u) != 0;
+    const bool odd_q = sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(q) & 2u) != 0;
+    if (!q) {
+      odd_p ? sums(No{}, Yes{}, No{}) : sums(No{}, No{}, No{});
+    } else if (odd_p) {
+      odd_q ? sums(Yes{}, Yes{}, Yes{}) : sums(Yes{}, Yes{}, No{});
+    } else {
+      odd_q ? sums(Yes{}, No{}, Yes{}) : sums(Yes{}, No{}, No{});
     }
+    if (whole < P.nseg && whole % nw == my)  // the row's end
+      put(whole, any_segment_part(p, q, hot, V, whole * P.seg, P.seg, lane, odd));
     cluster_sync();
 
     // every warp: the running sum over lanes' segments, kVerPer of them per lane
@@ -630,7 +722,7 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel
       hot = -1;
       continue;
     }
-    if (!(S > 0. && S < kVerHuge)) {
+    if (!(S > 0.)) {
       if (rank == 0 && threadIdx.x == 0) {
         P.tokens[b * (P.K + 1) + n] = -1;
         atomicOr(P.err, RLK_DEVERR_PROBS);
@@ -677,7 +769,7 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel
       int last = -1;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const double r = residual(pv[k], qv[k], bad);
+        const double r = residual<T>(pv[k], qv[k], odd);
         if (r > 0.) last = k;
         w[k] = k == 0 ? r : w[k > 0 ? k - 1 : 0] + r;
       }
