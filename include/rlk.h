@@ -363,8 +363,8 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
  * Writes tokens [B][K+1] int64 (the accepted drafts, the drawn token, then -1)
  * and num_accepted [B] int64.  A draft outside [0, V) within its sequence's
  * length is not accepted and sets RLK_DEVERR_TARGET; where r has no positive
- * entry, or its sum is not finite, the drawn token is -1 and RLK_DEVERR_PROBS
- * is set.  Strides may be 0 (shared rows).  K = 0 draws one token per sequence
+ * entry, or the row of p or of q that it is formed from holds a NaN or an
+ * infinity, the drawn token is -1 and RLK_DEVERR_PROBS is set.  Strides may be 0 (shared rows).  K = 0 draws one token per sequence
  * (draft_tokens, u_accept, draft_probs are not read).
  * Sizes: 1 <= V < 2^31, K < 2^20, B < 2^28.  B = 0 is a no-op.  One launch. */
 size_t rlk_sampling_workspace_bytes(void);

@@ -1257,7 +1257,8 @@ rlk_status check_distill(int64_t T, int64_t H, int64_t V, int64_t K, float tempe
                          float teacher_temperature, int logits_type) {
   rlk_status s = check_sizes(T, H, V, temperature);
   if (s != RLK_OK) return s;
-  if (K < 1 || !std::isfinite(teacher_temperature) || !(teacher_temperature > 0.f))
+  if (K < 1 || !std::isfinite(teacher_temperature) || !(teacher_temperature > 0.f) ||
+      !std::isfinite(1.f / teacher_temperature))
     return RLK_ERR_INVALID_ARG;
   if (logits_type != RLK_TYPE_BF16 && logits_type != RLK_TYPE_F32) return RLK_ERR_INVALID_ARG;
   return K > kDisMaxK ? RLK_ERR_UNSUPPORTED_SHAPE : RLK_OK;

@@ -63,6 +63,8 @@ def draft_verify(p, q, drafts, u_accept, u_sample, lens=None):
             if n < length:
                 if q is not None:
                     r = r - np.asarray(q[b, n], np.float64)
+                    if not np.isfinite(r).all():
+                        r = np.full(V, np.nan)
                 else:
                     r = r - (np.arange(V) == int(drafts[b, n]))
             r = np.where(r < 0, 0.0, r)

@@ -39,6 +39,7 @@ def test_argument_errors(L, call):
     for tau in (0.0, -1.0, float("nan"), float("inf")):
         assert call(L, tau=tau) == INVALID, tau
         assert call(L, tt=tau) == INVALID, tau
+    assert call(L, tt=1e-45) == INVALID            # 1 / tt overflows
     for k in ("h", "w", "ids", "g", "lse", "ws"):
         assert call(L, **{k: None}) == INVALID, k
     for k, off in (("h", 8), ("w", 2), ("ids", 4), ("g", 2), ("tl", 2), ("lse", 2)):

@@ -161,6 +161,23 @@ def test_probs_strides_in_place_and_leading_shapes():
     assert binding.rlk_token_probs(x[:0], 1.0).shape == (0, 170003)
 
 
+@pytest.mark.parametrize("src,dst", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+@pytest.mark.parametrize("V", [1, 5, 77, 4097, 60001])
+def test_probs_at_every_alignment(src, dst, V):
+    """The same bits wherever rows and outputs sit, and nothing written beside them."""
+    x = _logits(3, V, src, 13)
+    want = binding.rlk_token_probs(x, 0.8, dst)
+    for shift in range(9):
+        xs = torch.full((x.numel() + 24,), float("nan"), dtype=src, device="cuda")
+        xs[shift:shift + x.numel()] = x.view(-1)
+        ps = torch.full((x.numel() + 24,), 7.0, dtype=dst, device="cuda")
+        at = (shift * 5) % 9
+        out = ps[at:at + x.numel()].view(3, V)
+        binding.rlk_token_probs(xs[shift:shift + x.numel()].view(3, V), 0.8, out=out)
+        assert torch.equal(out, want)
+        assert (ps[:at] == 7).all() and (ps[at + x.numel():] == 7).all()
+
+
 def test_probs_offsets_past_32_bits():
     V, ld = 1000, (1 << 31) - 8
     base = torch.empty(ld + V, dtype=BF16, device="cuda")
@@ -297,6 +314,53 @@ def test_verify_bad_tokens_and_rows_without_a_distribution():
     assert got[0][0, got[1][0]] == -1 and got[0][1, 0] == -1
     for b in (3, 4, 5):
         assert torch.equal(got[0][b], good[0][b])
+    # in the draft's rows they matter where a draft is refused
+    for value in (float("nan"), float("inf")):
+        qn = q.clone()
+        qn[:, :, V - 1] = value
+        got = binding.rlk_draft_verify(p, qn, d, ua, us, workspace=ws)
+        _check_verify(p, qn, d, ua, us, None, got)
+        refused = got[1] < K
+        assert refused.any() and (got[0][refused, got[1][refused]] == -1).all()
+        assert binding.rlk_read_device_error(ws) == binding.RLK_DEVERR_PROBS
+
+
+def test_verify_subnormal_and_unnormalised_rows():
+    """Probabilities down to the smallest subnormals, and rows that sum to
+    anything: only their proportions count."""
+    B, V = 8, 1500
+    g = torch.Generator(device="cuda").manual_seed(9)
+    p = torch.rand(B, 2, V, generator=g, device="cuda")
+    p[0] *= 1e-42
+    p[1] = (p[1] * 4).floor() * 2.0 ** -149
+    p[2] *= 1e30
+    p[3, :, ::2] = 0
+    p[4, :, : V - 1] *= 1e-30
+    q = p[:, :1] * torch.rand(B, 1, V, generator=g, device="cuda") * 1.5
+    d = torch.full((B, 1), 3, device="cuda")
+    ua = torch.rand(B, 1, generator=g, device="cuda")
+    us = torch.rand(B, generator=g, device="cuda")
+    for ua_k in (ua, torch.ones_like(ua), torch.zeros_like(ua)):
+        _check_verify(p, q, d, ua_k, us, None, binding.rlk_draft_verify(p, q, d, ua_k, us))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_verify_writes_its_outputs_only_and_any_alignment(dtype):
+    B, K, V = 6, 3, 1537
+    p, q, d, ua, us, _ = _verify_case(B, K, V, dtype, 51)
+    ref = binding.rlk_draft_verify(p, q, d, ua, us)
+    room = torch.full((B * (K + 1) + 16,), 77, dtype=torch.int64, device="cuda")
+    count = torch.full((B + 16,), 77, dtype=torch.int64, device="cuda")
+    out = (room[8:8 + B * (K + 1)].view(B, K + 1), count[8:8 + B])
+    for shift in range(1, 9):                      # every offset of the rows within 16 bytes
+        ps = torch.empty(p.numel() + shift, dtype=dtype, device="cuda")[shift:].view(p.shape)
+        qs = torch.empty(q.numel() + 2 * shift, dtype=dtype, device="cuda")[2 * shift:].view(q.shape)
+        ps.copy_(p)
+        qs.copy_(q)
+        binding.rlk_draft_verify(ps, qs, d, ua, us, out=out)
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+        assert (room[:8] == 77).all() and (room[-8:] == 77).all()
+        assert (count[:8] == 77).all() and (count[-8:] == 77).all()
 
 
 def test_verify_strides():
