@@ -460,7 +460,8 @@ rlk_status enqueue_fwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
 // v0 = 0, Vloc = Vfull), chunked as the full head is.  dh_parts null: dHidden
 // accumulated over the chunks and written as bf16; else each chunk's fp32
 // product goes to dh_parts (EpiDh::kPart layout).  `dis`: the distillation's
-// dlogits, with its loss gradients, a bf16 dW or (dW null) none.
+// dlogits, with its loss gradients, a bf16 dW or (dW null) none; dx_all: room for
+// the dX of every chunk, for the order of few rows (then with dh_parts).
 rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t* targets,
                        int64_t T, int64_t H, int64_t Vloc, int64_t v0, int64_t Vfull,
                        float temperature, const float* lse, const float* entropy,
@@ -470,14 +471,17 @@ rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
                        uint64_t wait_limit_ns = kWaitLimitNs, int stall_first_h = 0,
                        uint32_t* chunk_done = nullptr, uint32_t seq = 0,
                        const DistillRows* dis = nullptr, const float* dloss = nullptr,
-                       bool dw_bf16 = false) {
+                       bool dw_bf16 = false, uint8_t* dx_all = nullptr) {
   BwdParams P;
-  P.plan = make_bwd_plan(T, H, Vloc, vchunk(Vfull), dW != nullptr);
+  P.plan = make_bwd_plan(T, H, Vloc, vchunk(Vfull), dW != nullptr, dx_all != nullptr);
   const BwdPlan& pl = P.plan;
+  // the chunks' dX buffers, or the one matrix of all chunks
   void* dx[kDxBuffers];
-  for (int i = 0; i < kDxBuffers; ++i) {
-    dx[i] = ws + L.dx[i];
-    if (!make_map(&P.maps.dx_st[i], dx[i], pl.ldx, T, pl.ldx, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+  const int nbuf = dx_all ? 1 : kDxBuffers;
+  const int64_t cols = dx_all ? static_cast<int64_t>(pl.NC) * pl.ldx : pl.ldx;
+  for (int i = 0; i < nbuf; ++i) {
+    dx[i] = dx_all ? dx_all : ws + L.dx[i];
+    if (!make_map(&P.maps.dx_st[i], dx[i], cols, T, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
       return RLK_ERR_CUDA;
   }
   // K-major operands of the recompute and dHidden units: one 2-D box per K
@@ -485,19 +489,18 @@ rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
   if (!map_kmajor(&P.maps.hid_k, hidden, H, T, H, kBM) ||
       !map_kmajor(&P.maps.w_k, W, H, Vloc, H, kBM))
     return RLK_ERR_CUDA;
-  for (int i = 0; i < kDxBuffers; ++i)
-    if (!map_kmajor(&P.maps.dx_k[i], dx[i], pl.ldx, T, pl.ldx, kBM)) return RLK_ERR_CUDA;
+  for (int i = 0; i < nbuf; ++i)
+    if (!map_kmajor(&P.maps.dx_k[i], dx[i], cols, T, cols, kBM)) return RLK_ERR_CUDA;
   // MN-major operands of the dHidden and dW units: 3-D maps (half the copies)
   // when the driver takes them, else 2-D maps; same shared-memory bytes.
   bool mn3 = map_mnmajor3(&P.maps.w_mn, W, H, Vloc, H) &&
              map_mnmajor3(&P.maps.hid_mn, hidden, H, T, H);
-  for (int i = 0; mn3 && i < kDxBuffers; ++i)
-    mn3 = map_mnmajor3(&P.maps.dx_mn[i], dx[i], pl.ldx, T, pl.ldx);
+  for (int i = 0; mn3 && i < nbuf; ++i) mn3 = map_mnmajor3(&P.maps.dx_mn[i], dx[i], cols, T, cols);
   if (!mn3) {
     if (!map_mnmajor(&P.maps.w_mn, W, H, Vloc, H) || !map_mnmajor(&P.maps.hid_mn, hidden, H, T, H))
       return RLK_ERR_CUDA;
-    for (int i = 0; i < kDxBuffers; ++i)
-      if (!map_mnmajor(&P.maps.dx_mn[i], dx[i], pl.ldx, T, pl.ldx)) return RLK_ERR_CUDA;
+    for (int i = 0; i < nbuf; ++i)
+      if (!map_mnmajor(&P.maps.dx_mn[i], dx[i], cols, T, cols)) return RLK_ERR_CUDA;
   }
   P.mn3 = mn3 ? 1 : 0;
   P.targets = targets;
@@ -529,7 +532,9 @@ rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
   P.seq = seq;
   P.dis = dis ? *dis : DistillRows{};
   P.dloss = dloss;
-  P.dw_bf16 = dw_bf16 ? 1 : 0;
+  P.dw_bf16 = dw_bf16 && dW ? 1 : 0;
+  if (P.dw_bf16 && !make_map(&P.maps.dw_st, dW, H, Vloc, H, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return RLK_ERR_CUDA;
 
   // (the distillation's counters are cleared before its preparation, behind which
   // this launch does not wait)
@@ -538,8 +543,9 @@ rlk_status enqueue_bwd(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t*
   // Units wait on units claimed earlier, and only running CTA pairs claim
   // units, so no pair ever waits on one that has not started: the launch needs
   // no co-residency guarantee.
-  return dis ? launch_pair<kModeBwdDistill>(P, pl.total, false, st, true)
-             : launch_pair<kModeBwd>(P, pl.total, false, st);
+  return !dis     ? launch_pair<kModeBwd>(P, pl.total, false, st)
+         : dx_all ? launch_pair<kModeBwdDistillFew>(P, pl.total, false, st, true)
+                  : launch_pair<kModeBwdDistill>(P, pl.total, false, st, true);
 }
 
 }  // namespace
@@ -980,6 +986,7 @@ __global__ void __launch_bounds__(256) dhidden_combine_kernel(const float* __res
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n4;
        i += stride) {
     float4 a = reinterpret_cast<const float4*>(parts)[i];
+#pragma unroll 8
     for (int k = 1; k < nparts; ++k) {
       const float4 v = reinterpret_cast<const float4*>(parts + k * count)[i];
       a.x = a.x + v.x;
@@ -1220,13 +1227,22 @@ rlk_status rlk_linear_logp_fwd_noalloc(const rlk_bf16* hidden, const rlk_bf16* W
 namespace rlk {
 namespace {
 
-// The sorted slots and their table behind a pass's own scratch, from `base`.
+// The sorted slots and their table behind a pass's own scratch, from `base`; in a
+// backward of few rows the dX of all chunks and their dHidden products.
 struct DistillLayout {
-  size_t ids, logq, y, sum, count, head, end;
+  size_t ids, logq, y, sum, count, head, dx, parts, end;
   int64_t G;
 };
 
-DistillLayout distill_layout(size_t base, int64_t T, int64_t V, int64_t K, int shift) {
+constexpr int64_t kFewTiles = 8192;
+constexpr int64_t kFewBytes = int64_t{256} << 20;
+
+bool distill_few(int64_t T, int64_t H, int64_t V) {
+  const int64_t nc = ceil_div(V, vchunk(V));
+  return nc > 1 && ceil_div(T, kPairM) * H <= kFewTiles && T * nc * vchunk(V) * 2 <= kFewBytes;
+}
+
+DistillLayout distill_layout(size_t base, int64_t T, int64_t H, int64_t V, int64_t K, int shift) {
   DistillLayout L;
   const size_t t = static_cast<size_t>(T), k = static_cast<size_t>(K);
   L.G = ceil_div(V, int64_t{1} << shift);
@@ -1236,7 +1252,13 @@ DistillLayout distill_layout(size_t base, int64_t T, int64_t V, int64_t K, int s
   L.sum = L.y + align256(t * k * 4);
   L.count = L.sum + align256(t * 4);
   L.head = L.count + align256(t * 4);
-  L.end = L.head + align256(t * static_cast<size_t>(L.G) * sizeof(uint2));
+  L.dx = L.head + align256(t * static_cast<size_t>(L.G) * sizeof(uint2));
+  L.parts = L.end = L.dx;
+  if (shift == kDisBwdShift && distill_few(T, H, V)) {
+    const size_t nc = static_cast<size_t>(ceil_div(V, vchunk(V)));
+    L.parts = L.dx + align256(t * nc * vchunk(V) * 2);
+    L.end = L.parts + align256(nc * t * H * 4);
+  }
   return L;
 }
 
@@ -1291,8 +1313,8 @@ size_t rlk_linear_distill_workspace_bytes(int64_t T, int64_t H, int64_t V, int64
                                           int for_backward) {
   if (check_distill(T, H, V, K, 1.f, 1.f, RLK_TYPE_F32) != RLK_OK) return 0;
   const Layout L = layout(T, H, V);
-  const size_t fwd = distill_layout(L.fwd_end, T, V, K, kDisFwdShift).end;
-  const size_t bwd = distill_layout(L.bwd_end, T, V, K, kDisBwdShift).end;
+  const size_t fwd = distill_layout(L.fwd_end, T, H, V, K, kDisFwdShift).end;
+  const size_t bwd = distill_layout(L.bwd_end, T, H, V, K, kDisBwdShift).end;
   return for_backward ? std::max(fwd, bwd) : fwd;
 }
 
@@ -1312,7 +1334,7 @@ rlk_status rlk_linear_distill_fwd(const rlk_bf16* hidden, const rlk_bf16* W,
       !aligned(teacher_lse, 4) || !aligned(loss, 4) || !aligned(lse, 4))
     return RLK_ERR_MISALIGNED;
   const Layout L = layout(T, H, V);
-  const DistillLayout DL = distill_layout(L.fwd_end, T, V, K, kDisFwdShift);
+  const DistillLayout DL = distill_layout(L.fwd_end, T, H, V, K, kDisFwdShift);
   if (workspace_bytes < DL.end) return RLK_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if ((s = check_device(&sms)) != RLK_OK) return s;
@@ -1372,7 +1394,7 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
       !aligned(lse, 4) || !aligned(dloss, 4))
     return RLK_ERR_MISALIGNED;
   const Layout L = layout(T, H, V);
-  const DistillLayout DL = distill_layout(L.bwd_end, T, V, K, kDisBwdShift);
+  const DistillLayout DL = distill_layout(L.bwd_end, T, H, V, K, kDisBwdShift);
   if (workspace_bytes < DL.end) return RLK_ERR_WORKSPACE_TOO_SMALL;
   if ((s = check_device(&sms)) != RLK_OK) return s;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1383,9 +1405,14 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
   if ((s = enqueue_distill_prep(teacher_ids, teacher_logits, logits_type, teacher_lse, T, V, K,
                                 teacher_temperature, kDisBwdShift, D, st)) != RLK_OK)
     return s;
-  return enqueue_bwd(hidden, W, nullptr, T, H, V, 0, V, temperature, lse, nullptr, nullptr, nullptr,
-                     dHidden, nullptr, 0, 0, static_cast<float*>(dW), ws, L, st, kWaitLimitNs, 0,
-                     nullptr, 0, &D, dloss, dW_type == RLK_TYPE_BF16);
+  const bool few = distill_few(T, H, V);
+  float* parts = few ? reinterpret_cast<float*>(ws + DL.parts) : nullptr;
+  if ((s = enqueue_bwd(hidden, W, nullptr, T, H, V, 0, V, temperature, lse, nullptr, nullptr, nullptr,
+                       dHidden, parts, T, pl.NC, static_cast<float*>(dW), ws, L, st, kWaitLimitNs, 0,
+                       nullptr, 0, &D, dloss, dW_type == RLK_TYPE_BF16,
+                       few ? ws + DL.dx : nullptr)) != RLK_OK)
+    return s;
+  return few ? rlk_dhidden_combine(parts, pl.NC, T * H, dHidden, stream) : RLK_OK;
 }
 
 }  // extern "C"

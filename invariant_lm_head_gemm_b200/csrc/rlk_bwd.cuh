@@ -43,6 +43,7 @@ struct BwdMaps {
   CUtensorMap dx_k[kDxBuffers];   // dX buffer [T, ldx], K-major, box 64 x 128
   CUtensorMap dx_mn[kDxBuffers];  // dX buffer read as MN-major (M = v, K = t), box 64 x 64 (x 2)
   CUtensorMap dx_st[kDxBuffers];  // dX buffer written by TMA stores, box 32 x 32, no swizzle
+  CUtensorMap dw_st;              // a bf16 dW [V,H] written by TMA stores (distillation), box 32 x 32
 };
 
 struct BwdPlan {
@@ -52,6 +53,7 @@ struct BwdPlan {
   int valid_last;        // vocab entries of the last chunk
   int KB_R;              // k-blocks of a recompute tile (H / 64)
   int KB_D;              // k-blocks of a dW tile (ceil(T / 64))
+  int few;               // the order for few rows (bwd_decode_few)
   long long total;       // number of units
 };
 
@@ -120,7 +122,7 @@ __host__ inline long long bwd_total_units(const BwdPlan& P);
 
 // Without dW (`with_dw` false) there are no D units.
 __host__ inline BwdPlan make_bwd_plan(int64_t T, int64_t H, int64_t V, int64_t ldx,
-                                      bool with_dw = true) {
+                                      bool with_dw = true, bool few = false) {
   BwdPlan p;
   p.T = static_cast<int>(T);
   p.H = static_cast<int>(H);
@@ -136,6 +138,7 @@ __host__ inline BwdPlan make_bwd_plan(int64_t T, int64_t H, int64_t V, int64_t l
   p.VT_last = with_dw ? (p.valid_last + kPairM - 1) / kPairM : 0;
   p.KB_R = static_cast<int>(H / kBK);
   p.KB_D = static_cast<int>((T + kBK - 1) / kBK);
+  p.few = few ? 1 : 0;
   p.total = bwd_total_units(p);
   return p;
 }
@@ -205,7 +208,29 @@ __host__ __device__ inline BwdUnit bwd_group_unit(const BwdPlan& P, int g, int r
   return bwd_seg_R(P, g + 2, r - d);
 }
 
+// Few rows (the distillation): dX holds every chunk (one [T, NC ldx] matrix), and
+// each chunk's dHidden product stands alone, so nothing but R(c) -> H(c), D(c) is
+// ordered: all R units, then all H units, then all D units.
+__host__ __device__ inline BwdUnit bwd_decode_few(const BwdPlan& P, int u) {
+  const int rfull = P.MT * P.RT_full, nr = rfull * (P.NC - 1) + P.MT * P.RT_last;
+  if (u < nr) {
+    const int c = u / rfull;
+    return bwd_seg_R(P, c, u - c * rfull);
+  }
+  u -= nr;
+  const int h = bwd_nH(P);
+  if (u < h * P.NC) return bwd_seg_H(P, u / h, u % h);
+  u -= h * P.NC;
+  const int dfull = P.NH * P.VT_full;
+  if (dfull > 0 && u < dfull * (P.NC - 1) + P.NH * P.VT_last) {
+    const int c = u / dfull;
+    return bwd_seg_D(P, c, u - c * dfull);
+  }
+  return BwdUnit{-1, 0, 0, 0};
+}
+
 __host__ __device__ inline BwdUnit bwd_decode(const BwdPlan& P, int u) {
+  if (P.few) return bwd_decode_few(P, u);
   for (int c = 0; c < 2 && c < P.NC; ++c) {
     const int n = bwd_nR(P, c);
     if (u < n) return bwd_seg_R(P, c, u);

@@ -172,6 +172,7 @@ struct EpiDistill {
     int T;
     int V;
     int c0;            // first W row of the chunk
+    int x0;            // the chunk's first column of the dX matrix
     float scale_log2;  // log2(e) / tau
     float inv_tau;
   };
@@ -227,7 +228,7 @@ struct EpiDistill {
         for (int j = 0; j < 32; ++j) dx[j] = (j == d) ? dx[j] - hit : dx[j];
       }
       __syncwarp();
-      if (any_row) store_dx_chunk(dx, store_map, stage + (c & 1) * 2048u, lane, loc0, warp_row0);
+      if (any_row) store_dx_chunk(dx, store_map, stage + (c & 1) * 2048u, lane, p.x0 + loc0, warp_row0);
     }
   }
 };

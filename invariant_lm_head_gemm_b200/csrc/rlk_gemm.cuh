@@ -459,27 +459,21 @@ struct EpiStore {
 
 // The same tile stored as bf16 (one rounding of the fp32 sum), where dW goes
 // straight into a bf16 gradient: half the bytes written, and no pass to convert.
+// Staged and stored like a dlogits chunk: 16-byte stores of a lane per row, 32 rows
+// apart, held a tile's epilogue for 5 us (few rows: nothing hides it).
 struct EpiStoreBf16 {
-  __device__ static void tile(__nv_bfloat16* out, int rows, int ncols, int ld, int row,
-                              uint32_t taddr, int nt) {
+  __device__ static void tile(const CUtensorMap* store_map, int row0, int ncols, uint32_t taddr,
+                              int nt, uint32_t stage, int lane) {
 #pragma unroll 1
     for (int c = 0; c < kBN / 32; ++c) {
       const int col0 = nt * kBN + c * 32;
-      if (col0 >= ncols) break;  // warp-uniform
+      if (col0 >= ncols) break;  // warp-uniform; ncols = H is a multiple of 64: a chunk is whole
       uint32_t r[32];
       tmem_ld32(taddr + c * 32, r);
-      if (row >= rows) continue;
-      // ncols = H is a multiple of 64: a chunk is whole
-      uint4* dst = reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * ld + col0);
+      float v[32];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint4 w;
-        w.x = pack_bf16x2(__uint_as_float(r[8 * q + 0]), __uint_as_float(r[8 * q + 1]));
-        w.y = pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]));
-        w.z = pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]));
-        w.w = pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7]));
-        dst[q] = w;
-      }
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+      store_dx_chunk(v, store_map, stage + (c & 1) * 2048u, lane, col0, row0);
     }
   }
 };

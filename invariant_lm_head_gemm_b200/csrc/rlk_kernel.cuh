@@ -39,10 +39,16 @@ constexpr uint32_t kPAStage = kSubK * kSubA;  // a stage's A: 32 KB
 constexpr uint32_t kPBStage = kSubK * kSubB;  // a stage's B: 32 KB
 constexpr int kRing = 4;                      // units in flight through the pair's broadcast ring
 
-enum : int { kModeFwd = 0, kModeBwd = 1, kModeGemm = 2, kModeFwdDistill = 3, kModeBwdDistill = 4 };
-constexpr int kModes = 5;
+enum : int { kModeFwd = 0, kModeBwd = 1, kModeGemm = 2, kModeFwdDistill = 3, kModeBwdDistill = 4,
+             kModeBwdDistillFew = 5 };
+constexpr int kModes = 6;
 constexpr bool is_fwd(int mode) { return mode == kModeFwd || mode == kModeFwdDistill; }
-constexpr bool is_bwd(int mode) { return mode == kModeBwd || mode == kModeBwdDistill; }
+constexpr bool is_bwd(int mode) {
+  return mode == kModeBwd || mode == kModeBwdDistill || mode == kModeBwdDistillFew;
+}
+constexpr bool is_distill(int mode) {
+  return mode == kModeFwdDistill || mode == kModeBwdDistill || mode == kModeBwdDistillFew;
+}
 
 // Shared memory per mode: three operand stages (192 KB); the backward's
 // dlogit epilogue adds 16 KB of TMA store staging (two 2 KB buffers per
@@ -106,6 +112,10 @@ template <>
 struct ModeArgs<kModeBwdDistill> {
   using type = BwdParams;
 };
+template <>
+struct ModeArgs<kModeBwdDistillFew> {
+  using type = BwdParams;
+};
 
 // What one unit loads and computes.
 struct Job {
@@ -124,6 +134,7 @@ struct Job {
   int a_row0;       // M coordinate of the tile's first row in A's tensor map
   int b_col0;       // N coordinate of the first tile's first column in B's map
   int bk0;          // K offset of B's map
+  int ak0;          // K offset of A's map (few-row backward: the chunk's columns of dX)
   int a_ext;        // M extent of A's map: boxes starting at or past it are skipped
   int b_ext;        // N extent of B's map
 };
@@ -145,6 +156,7 @@ __device__ __forceinline__ Job make_job(const FwdArgs& P, long long u) {
   j.a_row0 = j.mt * kPairM;
   j.b_col0 = j.nt * kBN;
   j.bk0 = 0;
+  j.ak0 = 0;
   j.a_ext = P.ep.T;
   j.b_ext = P.ep.V;
   return j;
@@ -169,6 +181,7 @@ __device__ __forceinline__ Job make_job(const GemmArgs& P, long long u) {
   j.a_row0 = j.mt * kPairM;
   j.b_col0 = j.nt * kBN;
   j.bk0 = 0;
+  j.ak0 = 0;
   j.a_ext = P.M;
   j.b_ext = P.N;
   return j;
@@ -184,9 +197,12 @@ __device__ __forceinline__ Job make_job(const BwdParams& P, long long u) {
   j.nt = un.b;
   j.ntiles = 1;
   j.bk0 = 0;
+  j.ak0 = 0;
   j.a3 = j.b3 = false;
   j.ak3 = j.bk3 = false;
-  const int buf = un.c % kDxBuffers;
+  // few rows: one dX matrix with all chunks' columns side by side
+  const int buf = pl.few ? 0 : un.c % kDxBuffers;
+  const int x0 = pl.few ? un.c * pl.ldx : 0;
   if (un.type == kUnitR) {
     j.kbs = pl.KB_R;
     j.a_mn = j.b_mn = false;
@@ -204,6 +220,7 @@ __device__ __forceinline__ Job make_job(const BwdParams& P, long long u) {
     j.mB = &P.maps.w_mn;
     j.b3 = P.mn3 != 0;
     j.a_row0 = un.a * kPairM;
+    j.ak0 = x0;
     j.b_col0 = un.b * kBN;
     j.bk0 = un.c * pl.ldx;
     j.a_ext = pl.T;
@@ -214,9 +231,9 @@ __device__ __forceinline__ Job make_job(const BwdParams& P, long long u) {
     j.mA = &P.maps.dx_mn[buf];
     j.mB = &P.maps.hid_mn;
     j.a3 = j.b3 = P.mn3 != 0;
-    j.a_row0 = un.a * kPairM;
+    j.a_row0 = x0 + un.a * kPairM;
     j.b_col0 = un.b * kBN;
-    j.a_ext = pl.ldx;
+    j.a_ext = x0 + pl.ldx;
     j.b_ext = pl.H;
   }
   return j;
@@ -465,7 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t dAs = dA + sub * kSubA, dBs = dB + sub * kSubB;
               const int k = sub == 0 ? k0 : k1;
               if (!j.a_mn) {
-                if (!j.ak3 && a0 < j.a_ext) tma_load_2d_pair(dAs, j.mA, fb, k, a0);
+                if (!j.ak3 && a0 < j.a_ext)
+                  tma_load_2d_pair(dAs, j.mA, fb, Mode == kModeBwdDistillFew ? j.ak0 + k : k, a0);
               } else if (j.a3) {
                 if (a0 < j.a_ext) tma_load_3d_pair(dAs, j.mA, fb, 0, k, a0 >> 6);
               } else {
@@ -548,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    constexpr bool kDistill = Mode == kModeFwdDistill || Mode == kModeBwdDistill;
+    constexpr bool kDistill = is_distill(Mode), kFew = Mode == kModeBwdDistillFew;
     if constexpr (kDistill) grid_dependency_wait();  // the teacher's rows
     const int q = warp & 3;
     const int row_in_tile = q * 32 + lane;
@@ -578,13 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool ok = mbar_wait_bounded(tfull_bar(acc), use & 1u, abort_flag, err, lim);
           if constexpr (is_bwd(Mode)) {
             const BwdPlan& pl = P.plan;
-            if (ok && j.type == kUnitR && j.c >= kDxBuffers) {
+            if (!kFew && ok && j.type == kUnitR && j.c >= kDxBuffers) {
               const int c3 = j.c - kDxBuffers;
               ok = wait_counter_bounded(P.bufdone + c3,
                                         2u * static_cast<uint32_t>(bwd_nH(pl) + bwd_nD(pl, c3)),
                                         abort_flag, err, lim);
             }
-            if (ok && j.type == kUnitH && j.c >= 1) {
+            if (!kFew && ok && j.type == kUnitH && j.c >= 1) {
               ok = wait_counter_bounded(
                   P.hdone + (static_cast<size_t>(j.c - 1) * pl.MT + j.mt) * pl.NH + j.nt, 2u,
                   abort_flag, err, lim);
@@ -617,11 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.T = pl.T;
               p.V = pl.V;
               p.c0 = j.c * pl.ldx;
+              p.x0 = kFew ? p.c0 : 0;
               p.scale_log2 = P.scale_log2;
               p.inv_tau = P.inv_tau;
               EpiDistill::State st;
               EpiDistill::begin_unit(p, st, row);
-              EpiDistill::tile(p, st, taddr, j.nt, &P.maps.dx_st[j.c % kDxBuffers],
+              EpiDistill::tile(p, st, taddr, j.nt, &P.maps.dx_st[kFew ? 0 : j.c % kDxBuffers],
                                sStage + q * 4096u, lane, row - lane);
             } else {
               EpiDlogits::Params p;
@@ -662,9 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             EpiDh::begin_unit(p, st, row, 0, 0);
             EpiDh::tile(p, st, taddr, j.nt);
           } else if (kDistill && P.dw_bf16 != 0) {
-            EpiStoreBf16::tile(reinterpret_cast<__nv_bfloat16*>(P.dW) +
-                                   static_cast<size_t>(j.c) * pl.ldx * pl.H,
-                               bwd_chunk_valid(pl, j.c), pl.H, pl.H, row, taddr, j.nt);
+            EpiStoreBf16::tile(&P.maps.dw_st, j.c * pl.ldx + row - lane, pl.H, taddr, j.nt,
+                               sStage + q * 4096u, lane);
           } else {
             EpiStore::Params p;
             p.out = P.dW + static_cast<size_t>(j.c) * pl.ldx * pl.H;
@@ -686,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if constexpr (is_bwd(Mode)) {
+          if (kFew && j.type != kUnitR) continue;  // nothing waits for these units
           if (j.type == kUnitR && lane == 0) bulk_wait_all();  // dX tiles written
           epilogue_bar();  // every store of this CTA's half of the unit is done or issued
           if (ep_leader) {
@@ -714,6 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (is_fwd(Mode)) {
         if (go) EpiFwd::end_unit(P.ep, fst, j.nt / P.group);
       }
+    }
+    if constexpr (kDistill && is_bwd(Mode)) {
+      if (lane == 0) bulk_wait_all();  // dW's stores read this CTA's shared memory
     }
   }
 
