@@ -1234,6 +1234,14 @@ struct DistillLayout {
   int64_t G;
 };
 
+// Whether the backward takes the order for few rows (rlk_bwd.cuh).  In the other one
+// a dHidden tile's chunks follow one another and three dX buffers go round, a chain
+// of recompute, dHidden, recompute, ... that takes its time however little there is
+// to do: 161 us at T = 513, H = 1024, V = 32768 and 149 at T = 31, H = 576, V = 54485
+// (frozen head), against 121 and 75 here.  With ceil(T / 256) H above 8192 the pairs
+// are busy either way (T = 1024, H = 4096, V = 151936: 3232 and 3114; T = 4000, H = 512,
+// V = 65536: 745 and 783) and the other order needs less memory: here all of dX, at
+// most kFewBytes, and 4 T H bytes per chunk of 8192.
 constexpr int64_t kFewTiles = 8192;
 constexpr int64_t kFewBytes = int64_t{256} << 20;
 

@@ -12,7 +12,15 @@
 // The logits come from the same tiles, in the same epilogue, as the lse: a row's
 // K logits cost one comparison per chunk and one select per hit (epilogue work
 // that hides under the tile's MMAs), where gathering them by K dot products per
-// row would read K rows of W for every row of hidden.
+// row would read K rows of W for every row of hidden.  Measured at T = 2047, H = 4096,
+// V = 32768: 390 us with 64 slots per row, 395 with none used (power-capped, one
+// process), tensor pipe 94% active; forward and backward at T = 5980, H = 4096,
+// V = 151936, K = 64: 23.4 ms, 1275 TFLOP/s of the 8 T H V that recompute makes it,
+// bound as the linear-logp kernels are.  Scoring 16 rows: 198 us, W's 1.25 GB at 0.96
+// of the measured copy rate.
+//
+// dX is rounded to bf16 for the two products, as in the linear-logp backward, so
+// gradients are off by about 1.7e-3 of their norm before their own rounding.
 #pragma once
 
 #include <cstdint>

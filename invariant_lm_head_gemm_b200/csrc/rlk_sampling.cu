@@ -66,10 +66,13 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_
 // take whole aligned vectors.
 //
 // Bound by HBM where there are many rows: each entry is read once and written
-// once, one CTA's copies running beside the other's looks.  Few instructions per
-// entry is what that takes: holding the entries in registers instead (one look,
-// one exponential, but 64 warps to a row of 50257, each with its reductions) ran
-// 55 instructions per entry and 128 us at 1027 x 50257 bf16.
+// once, one CTA's copies running beside another's looks.  320 x 151936 fp32: 74.5 us,
+// 5.2 TB/s, 0.80 of the measured copy; 1027 x 50257 bf16 (half the bytes per entry, as
+// many instructions): 45 us, 0.70; one row of 151936: 6.6 us.  Few instructions per
+// entry is what that takes: holding the entries in registers instead (one look, one
+// exponential, but 64 warps to a row of 50257, each with its reductions) ran 55
+// instructions per entry and 128 us at 1027 x 50257.  Persistent CTAs were slower
+// (90 us at 320 x 151936), and so were 512 and 128 threads (91, 84).
 constexpr int kProbMaxCluster = 8;
 constexpr int kProbThreads = 256;
 constexpr uint32_t kProbSlice = 100u * 1024u;  // bytes of a slice at most
@@ -472,8 +475,12 @@ __global__ void __launch_bounds__(kProbLongThreads) probs_long_kernel(const Prob
 // cluster's size, which follows the number of sequences.
 //
 // Bound by latency at few sequences (the drafts, their entries, the row, the
-// walk: four round trips and a cluster barrier), by instructions and then by HBM at
-// many.
+// walk: four round trips and a cluster barrier): one of 4 drafts and V = 151936 7.6 us.
+// At many, by HBM once those are over: 64 sequences 19.5 us, 78 MB of rows in 11 of
+// them; in bf16 (half the bytes per load) by the loads under way: 256 rows of 151936
+// 50 us, 3.1 TB/s.  What did not help: copies through shared memory ahead of the sums
+// (26 us at 64), several segments' loads at once or the next one's ahead in registers
+// (21), 256 threads (19.1, but 9.3 at one).
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerMaxCluster = 8;
