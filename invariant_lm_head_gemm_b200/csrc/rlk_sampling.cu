@@ -3,13 +3,11 @@
 // target's probabilities from given random numbers.
 //
 // Both are bound by the one pass over the rows they read (and, for the
-// probabilities, write).  A row is the work of one thread-block cluster whose
-// size follows from V alone: every sum then has an order that depends on V
-// only, so a row's results do not depend on how many rows there are or where
-// it sits.  Lanes take consecutive elements one by one, which coalesces at any
-// row alignment (an odd V puts every row at another offset) and keeps the
-// element-to-thread map, and with it the order of the sums, the same for all
-// rows.
+// probabilities, write), or at few rows by latency.  A row is the work of one
+// thread-block cluster.  Every sum takes the entries by their place in the row, in
+// an order that depends on V and the type only: not on how many rows there are, on
+// where the row sits, or on its alignment (an odd V puts every row at another
+// offset within 16 bytes).
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -97,7 +95,7 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// What every warp folds from the pairs of a row: its maximum and S (or, greedy,
+// What every warp folds from the pairs of a long row: its maximum and S (or, greedy,
 // the least index of the maximum).
 struct RowStats {
   float m, S;
@@ -156,8 +154,10 @@ __device__ __forceinline__ RowOut row_out(const RowStats& r, float tau, float k,
   return o;
 }
 
-// 2^(x k - c) or, where c = ref k is not finite, 2^((x - ref) k).  The rounding of
-// c is common to all entries and to their sum, and cancels between them.
+// A maximum's numerators: 2^(x k - c) with c = ref k as rounded, one operation per
+// entry.  The rounding of c, d = ref k - c, is common to all numerators and to their
+// sum and cancels between them; where |c| is so large that 2^d would matter on its
+// own (d reaches 2^-24 |c|), 2^((x - ref) k) instead.
 struct RowExp {
   float k, ref, c;
   bool plain;
@@ -165,11 +165,15 @@ struct RowExp {
     k = kk;
     ref = m == -INFINITY ? 0.f : m;  // -inf - -inf would be NaN
     c = ref * k;
-    plain = fabsf(c) < 1e30f;
+    plain = fabsf(c) < 1e6f;
   }
-  // for one maximum's numerators seen from another's
+  // the factor that takes this one's numerators to another's
   __device__ __forceinline__ float shift(const RowExp& to) const {
-    return plain && to.plain ? ex2_approx(c - to.c) : ex2_approx((ref - to.ref) * k);
+    if (plain && to.plain) return ex2_approx(c - to.c);
+    float e = (ref - to.ref) * k;
+    if (plain) e -= fmaf(ref, k, -c);
+    if (to.plain) e += fmaf(to.ref, k, -to.c);
+    return ex2_approx(e);
   }
 };
 
@@ -516,10 +520,10 @@ __device__ __forceinline__ double scaled(float x) {
   return __hiloint2double((u >> 3) & static_cast<int>(0x8fffffffu), sizeof(T) == 2 ? 0 : u << 29);
 }
 
-// max(0, p - q), scaled; `odd` becomes NaN where either is NaN or infinite.
+// max(0, p - q), scaled; `taint` becomes NaN where either is NaN or infinite.
 template <typename T>
-__device__ __forceinline__ double residual(float p, float q, float& odd) {
-  odd = fmaf(p, 0.f, fmaf(q, 0.f, odd));
+__device__ __forceinline__ double residual(float p, float q, float& taint) {
+  taint = fmaf(p, 0.f, fmaf(q, 0.f, taint));
   return scaled<T>(fmaxf(p, q)) - scaled<T>(q);
 }
 
@@ -576,7 +580,7 @@ __device__ __forceinline__ double tree8(const double (&r)[8]) {
 // per entry instead of 15).
 template <typename T, bool kQ, bool kOddP, bool kOddQ>
 __device__ __forceinline__ double segment_part(const T* p, const T* q, int lo, int seg, int lane,
-                                               float& odd) {
+                                               float& taint) {
   double acc = 0.;
   for (int o = lo; o < lo + seg; o += kVerPiece) {
     float pv[8], qv[8];
@@ -584,7 +588,7 @@ __device__ __forceinline__ double segment_part(const T* p, const T* q, int lo, i
     if constexpr (kQ) load_piece<kOddQ>(qv, q + o, o == 0, lane);
     double r[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = residual<T>(pv[j], kQ ? qv[j] : 0.f, odd);
+    for (int j = 0; j < 8; ++j) r[j] = residual<T>(pv[j], kQ ? qv[j] : 0.f, taint);
     acc += tree8(r);
   }
   return acc;
@@ -594,7 +598,7 @@ __device__ __forceinline__ double segment_part(const T* p, const T* q, int lo, i
 // one in it.
 template <typename T>
 __device__ __forceinline__ double any_segment_part(const T* p, const T* q, int hot, int V, int lo,
-                                                   int seg, int lane, float& odd) {
+                                                   int seg, int lane, float& taint) {
   double acc = 0.;
   for (int o = 0; o < seg; o += kVerPiece) {
     double r[8];
@@ -604,7 +608,7 @@ __device__ __forceinline__ double any_segment_part(const T* p, const T* q, int h
       const bool in = at < V - lo;
       const float pv = in ? to_f32(p[lo + at]) : 0.f;
       const float qv = in && q ? to_f32(q[lo + at]) : in && lo + at == hot ? 1.f : 0.f;
-      r[j] = residual<T>(pv, qv, odd);
+      r[j] = residual<T>(pv, qv, taint);
     }
     acc += tree8(r);
   }
@@ -670,12 +674,12 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel
   const int my = static_cast<int>(rank) * kVerWarps + warp;  // segments my, my + nw, ...
 
   for (int attempt = 0;; ++attempt) {
-    float odd = 0.f;
+    float taint = 0.f;
     if (attempt == 0) cluster_all_started();
     auto put = [&](int s, double acc) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
-      if (__any_sync(kFull, odd != 0.f)) acc = static_cast<double>(NAN);  // no distribution
+      if (__any_sync(kFull, taint != 0.f)) acc = static_cast<double>(NAN);  // no distribution
       if (lane < C)
         st_cluster_v2(mapa_shared(smem_u32(&totals[attempt][s]), lane),
                       static_cast<uint32_t>(__double2loint(acc)),
@@ -686,8 +690,8 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel
     auto sums = [&](auto kq, auto kp, auto kr) {
       for (int s = my; s < whole; s += nw) {
         put(s, kq.value || s != hot_seg
-                   ? segment_part<T, kq.value, kp.value, kr.value>(p, q, s * P.seg, P.seg, lane, odd)
-                   : any_segment_part(p, q, hot, V, s * P.seg, P.seg, lane, odd));
+                   ? segment_part<T, kq.value, kp.value, kr.value>(p, q, s * P.seg, P.seg, lane, taint)
+                   : any_segment_part(p, q, hot, V, s * P.seg, P.seg, lane, taint));
       }
     };
     using Yes = std::true_type;
@@ -702,7 +706,7 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel
       odd_q ? sums(Yes{}, No{}, Yes{}) : sums(Yes{}, No{}, No{});
     }
     if (whole < P.nseg && whole % nw == my)  // the row's end
-      put(whole, any_segment_part(p, q, hot, V, whole * P.seg, P.seg, lane, odd));
+      put(whole, any_segment_part(p, q, hot, V, whole * P.seg, P.seg, lane, taint));
     cluster_sync();
 
     // every warp: the running sum over lanes' segments, kVerPer of them per lane
@@ -776,7 +780,7 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel
       int last = -1;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const double r = residual<T>(pv[k], qv[k], odd);
+        const double r = residual<T>(pv[k], qv[k], taint);
         if (r > 0.) last = k;
         w[k] = k == 0 ? r : w[k > 0 ? k - 1 : 0] + r;
       }

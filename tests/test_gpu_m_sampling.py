@@ -104,6 +104,27 @@ def test_probs_masks_and_values_without_a_distribution(V):
     assert binding.rlk_read_device_error(ws) == binding.RLK_DEVERR_PROBS
 
 
+@pytest.mark.parametrize("V", [300, 60001, 151936, 230000])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_probs_of_far_off_logits(V, dtype):
+    """Rows far from zero, whole or in part: only differences count, however large
+    the logits (or a mask's -1e9) are beside them."""
+    base = _logits(8, V, F32, 15)
+    t = [1.0, 0.5, 1.0, 1.0, 1.0, 0.01, 1.0, 1.0]
+    off = [1e3, -3e5, 693147.0, -693140.0, -1e9, 1e4, 1e20, -2e38]
+    x = base + torch.tensor(off, device="cuda")[:, None]
+    x[2, V // 2:] -= 200.0                         # slices on both sides of the switch of form
+    x[3, : V // 2] += 64.0
+    x = x.to(dtype)
+    got = binding.rlk_token_probs(x, torch.tensor(t, device="cuda"), F32)
+    _check_probs(x.float().cpu().numpy(), t, got, F32)
+    masked = _logits(2, V, F32, 16)
+    masked[0, 3:] = -1e9
+    masked[1, : V - 2] = -1e38
+    _check_probs(masked.cpu().numpy(), [1.0, 0.3], binding.rlk_token_probs(
+        masked, torch.tensor([1.0, 0.3], device="cuda")), F32)
+
+
 def test_probs_row_temperatures_that_are_none():
     x = _logits(6, 3001, F32, 8)
     t = [-1.0, float("nan"), float("inf"), 1e-45, 1.0, 0.0]
