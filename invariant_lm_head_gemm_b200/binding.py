@@ -570,6 +570,7 @@ def rlk_transition_logp(x, v, prev, a, c, s, want_mean=False, out=None, workspac
 
 
 _TYPE_IDS = {torch.bfloat16: 0, torch.float32: 1}  # RLK_TYPE_*
+_BF16, _FP32, _INT64 = (torch.bfloat16,), (torch.float32,), (torch.int64,)
 
 
 def _on_stream(fn, dev, stream, *args):
@@ -586,7 +587,7 @@ def _on_stream(fn, dev, stream, *args):
 
 
 def _on(dev, t, dtypes, name, shape):
-    if t.device != dev or t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype not in dtypes or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" %
                          (name, " or ".join(str(d) for d in dtypes), list(shape), dev))
 
@@ -649,7 +650,7 @@ def rlk_token_probs(logits, temperature=1.0, dtype=None, out=None, workspace=Non
     row_t = None
     if isinstance(temperature, torch.Tensor):
         row_t, temperature = temperature, 1.0
-        _on(dev, row_t, (torch.float32,), "temperature", tuple(logits.shape[:-1]))
+        _on(dev, row_t, _FP32, "temperature", logits.shape[:-1])
     if (dtype or logits.dtype) not in _TYPE_IDS:
         raise ValueError("dtype must be bf16 or fp32")
     if out is not None and (out.device != dev or out.shape != logits.shape or
@@ -659,14 +660,17 @@ def rlk_token_probs(logits, temperature=1.0, dtype=None, out=None, workspace=Non
 
 
 def _token_probs(logits, ld, temperature, row_t, dtype, out, workspace, stream):
-    V = logits.shape[-1]
+    V = ld_out = logits.shape[-1]
     if out is None:
-        out = torch.empty_like(logits, dtype=dtype, memory_format=torch.contiguous_format)
+        out = torch.empty_like(logits, dtype=dtype) if logits.is_contiguous() else \
+            logits.new_empty(logits.shape, dtype=dtype)
+    else:
+        ld_out = _row_stride(out, "out")
     ws = sampling_workspace(logits.device) if workspace is None else _scratch(workspace, logits.device)
     _check(_samp().rlk_token_probs(
         logits.data_ptr(), _TYPE_IDS[logits.dtype], logits.numel() // V, V, ld, temperature,
         None if row_t is None else row_t.data_ptr(), out.data_ptr(), _TYPE_IDS[out.dtype],
-        _row_stride(out, "out"), ws.data_ptr(), ws.numel(), stream), "rlk_token_probs")
+        ld_out, ws.data_ptr(), ws.numel(), stream), "rlk_token_probs")
     return out
 
 
@@ -678,43 +682,45 @@ def rlk_draft_verify(target_probs, draft_probs, draft_tokens, u_accept, u_sample
     draft_tokens [B, K] int64; u_accept [B, K] and u_sample [B] fp32 uniform
     numbers in [0, 1); draft_lens [B] int64.  tokens holds the accepted drafts,
     the token drawn after them, then -1."""
-    dev = target_probs.device
     if target_probs.dim() != 3 or not target_probs.is_cuda or target_probs.dtype not in _TYPE_IDS:
         raise ValueError("target_probs must be a CUDA bf16 or fp32 tensor [B, K+1, V]")
-    B, K, V = target_probs.shape
-    K -= 1
-    if K < 0 or V < 1:
+    dev = target_probs.device
+    B, K1, V = target_probs.shape
+    if K1 < 1 or V < 1:
         raise ValueError("target_probs must be [B, K+1, V] with V >= 1")
-    if V > 1 and target_probs.stride(2) != 1:
+    p_strides = target_probs.stride()
+    if V > 1 and p_strides[2] != 1:
         raise ValueError("target_probs must have contiguous rows")
+    q_strides = (0, 0, 1)
     if draft_probs is not None:
+        q_strides = draft_probs.stride()
         if draft_probs.device != dev or draft_probs.dtype != target_probs.dtype or \
-                tuple(draft_probs.shape) != (B, K, V) or (V > 1 and draft_probs.stride(2) != 1):
+                draft_probs.shape != (B, K1 - 1, V) or (V > 1 and q_strides[2] != 1):
             raise ValueError("draft_probs must be [B, K, V] of target_probs' type and device, "
                              "with contiguous rows")
-    _on(dev, draft_tokens, (torch.int64,), "draft_tokens", (B, K))
-    _on(dev, u_accept, (torch.float32,), "u_accept", (B, K))
-    _on(dev, u_sample, (torch.float32,), "u_sample", (B,))
+    _on(dev, draft_tokens, _INT64, "draft_tokens", (B, K1 - 1))
+    _on(dev, u_accept, _FP32, "u_accept", (B, K1 - 1))
+    _on(dev, u_sample, _FP32, "u_sample", (B,))
     if draft_lens is not None:
-        _on(dev, draft_lens, (torch.int64,), "draft_lens", (B,))
+        _on(dev, draft_lens, _INT64, "draft_lens", (B,))
     if out is not None:
-        _on(dev, out[0], (torch.int64,), "tokens", (B, K + 1))
-        _on(dev, out[1], (torch.int64,), "num_accepted", (B,))
-    return _on_stream(_draft_verify, dev, stream, target_probs, draft_probs, draft_tokens, u_accept,
-                      u_sample, draft_lens, out, workspace)
+        _on(dev, out[0], _INT64, "tokens", (B, K1))
+        _on(dev, out[1], _INT64, "num_accepted", (B,))
+    return _on_stream(_draft_verify, dev, stream, target_probs, p_strides, draft_probs, q_strides,
+                      draft_tokens, u_accept, u_sample, draft_lens, out, workspace)
 
 
-def _draft_verify(p, q, draft_tokens, u_accept, u_sample, draft_lens, out, workspace, stream):
+def _draft_verify(p, p_strides, q, q_strides, draft_tokens, u_accept, u_sample, draft_lens, out,
+                  workspace, stream):
     B, K1, V = p.shape
-    tokens, accepted = out or (draft_tokens.new_empty((B, K1)), draft_tokens.new_empty(B))
+    tokens, accepted = out or (draft_tokens.new_empty((B, K1)),
+                               torch.empty_like(u_sample, dtype=torch.int64))
     ws = sampling_workspace(p.device) if workspace is None else _scratch(workspace, p.device)
-    p_sb, p_sk, _ = p.stride()
-    q_sb, q_sk, _ = (0, 0, 0) if q is None else q.stride()
     _check(_samp().rlk_draft_verify(
-        p.data_ptr(), p_sb, p_sk, None if q is None else q.data_ptr(), q_sb, q_sk, _TYPE_IDS[p.dtype],
-        draft_tokens.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
-        None if draft_lens is None else draft_lens.data_ptr(), B, K1 - 1, V, tokens.data_ptr(),
-        accepted.data_ptr(), ws.data_ptr(), ws.numel(), stream), "rlk_draft_verify")
+        p.data_ptr(), p_strides[0], p_strides[1], None if q is None else q.data_ptr(), q_strides[0],
+        q_strides[1], _TYPE_IDS[p.dtype], draft_tokens.data_ptr(), u_accept.data_ptr(),
+        u_sample.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(), B, K1 - 1, V,
+        tokens.data_ptr(), accepted.data_ptr(), ws.data_ptr(), ws.numel(), stream), "rlk_draft_verify")
     return tokens, accepted
 
 
@@ -757,11 +763,11 @@ def _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse):
     if W.dim() != 2 or teacher_ids.dim() != 2:
         raise ValueError("W must be [V, H] and teacher_ids [T, K]")
     V, K = W.shape[0], teacher_ids.shape[1]
-    _on(dev, W, (torch.bfloat16,), "W", (V, H))
-    _on(dev, teacher_ids, (torch.int64,), "teacher_ids", (T, K))
+    _on(dev, W, _BF16, "W", (V, H))
+    _on(dev, teacher_ids, _INT64, "teacher_ids", (T, K))
     _on(dev, teacher_logits, tuple(_TYPE_IDS), "teacher_logits", (T, K))
     if teacher_lse is not None:
-        _on(dev, teacher_lse, (torch.float32,), "teacher_lse", (T,))
+        _on(dev, teacher_lse, _FP32, "teacher_lse", (T,))
     return dev, (T, H, V, K)
 
 
@@ -775,8 +781,8 @@ def rlk_linear_distill_fwd(hidden, W, teacher_ids, teacher_logits, temperature=1
     log-sum-exp instead of renormalising over the slots."""
     dev, sizes = _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse)
     if out is not None:
-        _on(dev, out[0], (torch.float32,), "loss", sizes[:1])
-        _on(dev, out[1], (torch.float32,), "lse", sizes[:1])
+        _on(dev, out[0], _FP32, "loss", sizes[:1])
+        _on(dev, out[1], _FP32, "lse", sizes[:1])
     if teacher_temperature is None:
         teacher_temperature = temperature
     return _on_stream(_distill_fwd, dev, stream, sizes, hidden, W, teacher_ids, teacher_logits,
@@ -804,12 +810,12 @@ def rlk_linear_distill_bwd(hidden, W, teacher_ids, teacher_logits, temperature, 
     forward's lse; dW in dW_dtype (fp32 or bf16), or None for a frozen head."""
     dev, sizes = _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse)
     T, H, V, _ = sizes
-    _on(dev, lse, (torch.float32,), "lse", (T,))
-    _on(dev, dloss, (torch.float32,), "dloss", (T,))
+    _on(dev, lse, _FP32, "lse", (T,))
+    _on(dev, dloss, _FP32, "dloss", (T,))
     if dW_dtype is not None and dW_dtype not in _TYPE_IDS:
         raise ValueError("dW_dtype must be fp32, bf16 or None")
     if out is not None:
-        _on(dev, out[0], (torch.bfloat16,), "dHidden", (T, H))
+        _on(dev, out[0], _BF16, "dHidden", (T, H))
         if (out[1] is None) != (dW_dtype is None):
             raise ValueError("out must hold dW where dW_dtype is given, and only there")
         if out[1] is not None:
