@@ -413,6 +413,17 @@ def test_verify_offsets_past_32_bits():
 
 # ------------------------------------------------------------------ calls
 
+def test_many_short_rows():
+    x = _logits(100003, 5, F32, 17)
+    got = binding.rlk_token_probs(x, 0.9)
+    want = torch.softmax(x.double() / float(np.float32(0.9)), 1)
+    assert ((got.double() - want).abs() <= want * 300 * EPS).all()
+    c = _verify_case(20011, 2, 9, BF16, 18, True)
+    tok, n = binding.rlk_draft_verify(*c)
+    sel = torch.randperm(20011, device="cuda")[:300]
+    _check_verify(*[t[sel].contiguous() for t in c], (tok[sel], n[sel]))
+
+
 def test_binding_refusals():
     x = torch.zeros(2, 8, device="cuda")
     for bad in (lambda: binding.rlk_token_probs(x.double()),

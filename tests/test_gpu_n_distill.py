@@ -118,6 +118,8 @@ SHAPES = [
     (33, 128, 2000, 64), (64, 256, 1024, 8), (100, 192, 8193, 33), (224, 64, 1537, 100),
     (256, 64, 4097, 256), (257, 64, 1000, 7), (300, 256, 8192, 128), (513, 128, 8500, 32),
     (700, 64, 17000, 16),
+    # few rows over several vocabulary chunks
+    (1, 64, 8193, 3), (2, 128, 20000, 9), (3, 64, 151936, 40), (257, 320, 16385, 20),
 ]
 
 
@@ -130,7 +132,7 @@ def test_matches_the_oracle(T, H, V, K, tail):
     loss, lse, dH, dW, err = _run(*c, tau, tau_t)
     assert err == 0
     _check(ref, loss, lse, dH, dW, frob=T >= 64)
-    if T > 3:
+    if T > 3:  # the rows that _case leaves without a weight
         assert loss[1] == 0 and loss[2] == 0
         assert (dH[1:3] == 0).all()
 
@@ -278,6 +280,21 @@ def test_autograd(frozen):
         assert torch.equal(w2.grad, w.grad + w.grad)
 
 
+def test_autograd_without_and_with_one_gradient():
+    T, H, V, K = 40, 64, 9000, 6
+    hidden, W, ids, logits, lse, _ = _case(T, H, V, K, 56, tail=True)
+    want = _run(hidden, W, ids, logits, lse, torch.ones(T, device="cuda"), 1.0, 1.0, BF16)
+    with torch.no_grad():
+        loss = binding.LinearDistill.apply(hidden.requires_grad_(True), W, ids, logits, 1.0, None, lse)
+    assert not loss.requires_grad and torch.equal(loss, want[0])
+    w = W.clone().requires_grad_(True)
+    loss = binding.LinearDistill.apply(hidden.detach(), w, ids, logits, 1.0, None, lse)
+    loss.backward(torch.ones(1, device="cuda").expand(T), retain_graph=True)
+    assert torch.equal(w.grad, want[3])
+    loss.sum().backward()                          # the saved workspace serves a second pass
+    assert torch.equal(w.grad, want[3] + want[3])
+
+
 @pytest.mark.parametrize("T", [20, 300])
 def test_capture_and_side_stream(T):
     H, V, K = 64, 9000, 8
@@ -318,6 +335,36 @@ def test_capture_and_side_stream(T):
     loss, _ = binding.rlk_linear_distill_fwd(hidden, W, ids, logits, 1.0, teacher_lse=lse, stream=side)
     side.synchronize()
     assert torch.equal(loss, want[0])
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU, each with its own workspace (and, for the
+    sampling calls, one between them)."""
+    cases = [_case(T, 256, 20000, 12, 80 + T, tail=True) for T in (60, 700)]
+    want = [_run(*c, 1.0, 1.0, BF16) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [binding.make_distill_workspace(c[0].shape[0], 256, 20000, 12) for c in cases]
+    shared = binding.sampling_workspace()
+    x = torch.randn(50, 20000, device="cuda")
+    p = binding.rlk_token_probs(x, 1.0)
+    torch.cuda.synchronize()
+    got = [None, None]
+    probs = [None, None]
+    for _ in range(4):
+        for i, (c, st) in enumerate(zip(cases, streams)):
+            hidden, W, ids, logits, lse, dloss = c
+            loss, s = binding.rlk_linear_distill_fwd(hidden, W, ids, logits, 1.0, teacher_lse=lse,
+                                                     workspace=spaces[i], stream=st)
+            got[i] = (loss, s) + binding.rlk_linear_distill_bwd(
+                hidden, W, ids, logits, 1.0, s, dloss, teacher_lse=lse, workspace=spaces[i],
+                dW_dtype=BF16, stream=st)
+            probs[i] = binding.rlk_token_probs(x, 1.0, workspace=shared, stream=st)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+    assert all(torch.equal(q, p) for q in probs)
+    assert all(binding.rlk_read_device_error(w) == 0 for w in spaces + [shared])
 
 
 @pytest.mark.parametrize("T,H,V,K", [(19, 64, 513, 5), (250, 128, 9000, 40), (300, 64, 8500, 33)])
