@@ -392,12 +392,31 @@ rlk_status enqueue_fwd_partials_short(const rlk_bf16* hidden, const rlk_bf16* W,
   return launch_short(a, false, st, false, dis != nullptr);
 }
 
+// Whether the forward of T <= kDecMaxT rows that distils takes the pair kernel (to the
+// same bits).  The short-batch kernel streams W without padding T to 256 rows, but
+// hands each row's triple from warp to warp and CTA to CTA, 16 chunks to a split;
+// where W is small that chain, not W, is its time.  Estimates in us of both, from
+// rounds over their units (74 pairs, 33 clusters):
+//   pair:  8 + rounds max(6.5, 0.0128 H), a third more below 16 rows
+//   short: 16 + rounds (3 + 0.0043 H) + T (0.012 + 0.033 rounds)
+// and the pair kernel only where it is a tenth ahead.  Measured, short / pair, at
+// T = 64: H 256 V 1024 24 / 17, H 256 V 50000 32 / 22, H 1024 V 20000 30 / 20; at T = 256:
+// H 512 V 151936 128 / 53, H 1024 V 80000 86 / 47, H 4096 V 20000 73 / 55; the other way
+// at T = 33: H 4096 V 5000 36 / 46, H 4096 V 151936 205 / 266.
+bool distill_by_pairs(int64_t T, int64_t H, int64_t V) {
+  const double ng = static_cast<double>(fwd_groups(V)), h = static_cast<double>(H);
+  const double rp = std::ceil(ng / 74), rs = std::ceil(ng / 33);
+  const double pair = (8 + rp * std::max(6.5, 0.0128 * h)) * (T < 16 ? 1.35 : 1.);
+  const double chain = 16 + rs * (3 + 0.0043 * h) + static_cast<double>(T) * (0.012 + 0.033 * rs);
+  return pair < 0.9 * chain;
+}
+
 rlk_status enqueue_fwd_partials(const rlk_bf16* hidden, const rlk_bf16* W, const int64_t* targets,
                                 int64_t T, int64_t H, int64_t Vloc, int64_t v0, float temperature,
                                 float* part_m, float* part_s, float* part_b, int64_t ldp,
                                 float* ytgt, uint32_t* err, cudaStream_t st,
                                 const DistillRows* dis = nullptr) {
-  if (T <= kDecMaxT)
+  if (T <= kDecMaxT && !(dis && distill_by_pairs(T, H, Vloc)))
     return enqueue_fwd_partials_short(hidden, W, targets, T, H, Vloc, v0, temperature, part_m,
                                       part_s, part_b, ldp, ytgt, err, st, kWaitLimitNs, 0, dis);
   FwdArgs a;

@@ -113,7 +113,10 @@ def _run(hidden, W, ids, logits, lse, dloss, tau, tau_t, dW_dtype=F32, ws=None):
 
 
 SHAPES = [
-    # T, H, V, K: both short-batch forms, the pair kernel, ragged vocabularies, chunk borders
+    # T, H, V, K: the short-batch kernel in its forms (a large H and a small vocabulary)
+    (1, 4096, 513, 5), (16, 4096, 1500, 8), (32, 4096, 600, 20), (40, 4096, 3000, 33), (130, 4096, 2000, 64),
+    (250, 4096, 1100, 16),
+    # the pair kernel, ragged vocabularies, chunk borders
     (1, 64, 1, 1), (1, 256, 1000, 1), (2, 64, 31, 8), (16, 128, 513, 20), (17, 64, 700, 5),
     (33, 128, 2000, 64), (64, 256, 1024, 8), (100, 192, 8193, 33), (224, 64, 1537, 100),
     (256, 64, 4097, 256), (257, 64, 1000, 7), (300, 256, 8192, 128), (513, 128, 8500, 32),
@@ -137,9 +140,9 @@ def test_matches_the_oracle(T, H, V, K, tail):
         assert (dH[1:3] == 0).all()
 
 
-@pytest.mark.parametrize("T", [5, 40, 129, 600])
-def test_many_ids_in_one_chunk(T):
-    c = _case(T, 64, 3001, 60, T, near=True, unused=False)
+@pytest.mark.parametrize("T,H", [(5, 64), (40, 64), (129, 64), (600, 64), (7, 4096), (40, 4096), (129, 4096)])
+def test_many_ids_in_one_chunk(T, H):
+    c = _case(T, H, 3001, 60, T, near=True, unused=False)
     _check(_Ref(*c, 1.0, 1.0), *_run(*c, 1.0, 1.0)[:4], frob=False)
 
 
@@ -159,9 +162,10 @@ def test_dw_types_and_the_frozen_head(T, dW_dtype):
 
 
 @pytest.mark.parametrize("T", [3, 50, 250, 400])
-def test_lse_and_loss_are_those_of_linear_logp(T):
+@pytest.mark.parametrize("H", [256, 4096])
+def test_lse_and_loss_are_those_of_linear_logp(T, H):
     """One certain slot per row is the cross entropy of linear-logp."""
-    H, V = 256, 5000
+    V = 5000
     hidden, W, ids, _, _, _ = _case(T, H, V, 1, 9, unused=False)
     loss, lse = binding.rlk_linear_distill_fwd(hidden, W, ids, torch.zeros(T, 1, device="cuda"), 0.9)
     logp, _, lse2 = binding.rlk_linear_logp_fwd(hidden, W, ids[:, 0].contiguous(), 0.9)
