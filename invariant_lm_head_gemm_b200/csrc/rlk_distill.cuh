@@ -33,8 +33,11 @@ namespace rlk {
 // table of where every 2^shift columns' slots begin, Q and the count.  A rank
 // sort: at most K^2 / 32 comparisons per lane, from shared memory, beside the
 // T x H x V product it prepares.  Sums run over the sorted slots, so a row's
-// results do not depend on the order in which its slots are given.  The kernel
-// that reads all this is let in at once: only its epilogue has to wait.
+// results do not depend on the order in which its slots are given.  Without the
+// teacher's own lse, log q = (g - max g) / tau - log sum e^((g - max g) / tau): the
+// lse itself, max g / tau + log sum, would round to the size of the logits (half
+// a step at 65536 is 4e-3), and that error would scale all of the row's weights.  The
+// kernel that reads all this is let in at once: only its epilogue has to wait.
 template <typename TLogit>
 __global__ void __launch_bounds__(128) distill_prep_kernel(
     const int64_t* __restrict__ ids, const TLogit* __restrict__ logits,
@@ -53,12 +56,12 @@ __global__ void __launch_bounds__(128) distill_prep_kernel(
   for (int k0 = 0; k0 < K; k0 += 32) {
     const int k = k0 + lane;
     int id = -1;
-    float a = 0.f;
+    float logit = 0.f;
     if (k < K) {
       const int64_t i = ids[static_cast<size_t>(t) * K + k];
       if (i >= 0 && i < V) {
         id = static_cast<int>(i);
-        a = static_cast<float>(logits[static_cast<size_t>(t) * K + k]) / tau;
+        logit = static_cast<float>(logits[static_cast<size_t>(t) * K + k]);
       } else {
         bad |= i != -1;
       }
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(128) distill_prep_kernel(
     if (id >= 0) {
       const int at = n + __popc(used & ((1u << lane) - 1u));
       key[w][at] = id;
-      val[w][at] = a;
+      val[w][at] = logit;
     }
     n += __popc(used);
   }
@@ -94,20 +97,21 @@ __global__ void __launch_bounds__(128) distill_prep_kernel(
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   nan = __any_sync(0xffffffffu, nan);
   if (m == -INFINITY && !nan) n = 0;  // every slot at -inf: no weight anywhere
-  float L;
+  float ref = 0.f, L;  // log q = (g - ref) / tau - L
   if (teacher_lse != nullptr) {
     L = teacher_lse[t];
   } else {
+    ref = m;
     float s = 0.f;
-    for (int i = lane; i < n; i += 32) s += expf(sval[w][i] - m);
+    for (int i = lane; i < n; i += 32) s += expf((sval[w][i] - ref) / tau);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    L = m + logf(s);
+    L = logf(s);
   }
   const size_t row0 = static_cast<size_t>(t) * D.ld;
   float Q = 0.f;
   for (int i = lane; i < n; i += 32) {
-    const float logq = sval[w][i] - L;
+    const float logq = (sval[w][i] - ref) / tau - L;
     Q += dis_weight(logq);
     D.ids[row0 + i] = skey[w][i];
     D.logq[row0 + i] = logq;
