@@ -309,9 +309,11 @@ rlk_status rlk_transition_logp(const float* x, const float* v, const float* prev
  *    products.  T = 0 zeroes dW.
  *  - Workspace: rlk_linear_distill_workspace_bytes (0 for unsupported sizes), its
  *    first 256 bytes zeroed once; one buffer serves both passes, which keep
- *    nothing in it between them.  Calls that share a workspace must not overlap
- *    on the GPU (two streams, or two captured graphs replayed at once, need one
- *    each). */
+ *    nothing in it between them.  One sized for T, H, V and K serves every call
+ *    none of whose sizes is larger: for some of few rows the size holds room for
+ *    a faster order of the backward, which a smaller workspace does without, to
+ *    the same bits.  Calls that share a workspace must not overlap on the GPU (two
+ *    streams, or two captured graphs replayed at once, need one each). */
 size_t rlk_linear_distill_workspace_bytes(int64_t T, int64_t H, int64_t V, int64_t K,
                                           int for_backward);
 rlk_status rlk_linear_distill_fwd(const rlk_bf16* hidden, const rlk_bf16* W,

@@ -746,8 +746,8 @@ def _dis():
 
 
 def make_distill_workspace(T: int, H: int, V: int, K: int, for_backward: bool = True, device=None):
-    """A workspace tensor (uint8) for the distillation of T rows with K slots,
-    its error word zeroed."""
+    """A workspace tensor (uint8) for the distillation of up to T rows with up to K
+    slots, its error word zeroed."""
     n = int(_dis().rlk_linear_distill_workspace_bytes(T, H, V, K, 1 if for_backward else 0))
     if n == 0:
         raise ValueError("unsupported sizes T=%d H=%d V=%d K=%d" % (T, H, V, K))

@@ -1246,10 +1246,11 @@ rlk_status rlk_linear_logp_fwd_noalloc(const rlk_bf16* hidden, const rlk_bf16* W
 namespace rlk {
 namespace {
 
-// The sorted slots and their table behind a pass's own scratch, from `base`; in a
-// backward of few rows the dX of all chunks and their dHidden products.
+// The sorted slots and their table behind a pass's own scratch, from `base`, up to
+// `least`: what the pass needs; in a backward of few rows the dX of all chunks and
+// their dHidden products, up to `end`: what its order for few rows takes.
 struct DistillLayout {
-  size_t ids, logq, y, sum, count, head, dx, parts, end;
+  size_t ids, logq, y, sum, count, head, dx, parts, least, end;
   int64_t G;
 };
 
@@ -1260,7 +1261,9 @@ struct DistillLayout {
 // (frozen head), against 121 and 75 here.  With ceil(T / 256) H above 8192 the pairs
 // are busy either way (T = 1024, H = 4096, V = 151936: 3232 and 3114; T = 4000, H = 512,
 // V = 65536: 745 and 783) and the other order needs less memory: here all of dX, at
-// most kFewBytes, and 4 T H bytes per chunk of 8192.
+// most kFewBytes, and 4 T H bytes per chunk of 8192.  Both give the same bits, so a
+// workspace that has no room for that (one sized for more rows than this order is
+// for can be the smaller one) gets the other order.
 constexpr int64_t kFewTiles = 8192;
 constexpr int64_t kFewBytes = int64_t{256} << 20;
 
@@ -1280,7 +1283,7 @@ DistillLayout distill_layout(size_t base, int64_t T, int64_t H, int64_t V, int64
   L.count = L.sum + align256(t * 4);
   L.head = L.count + align256(t * 4);
   L.dx = L.head + align256(t * static_cast<size_t>(L.G) * sizeof(uint2));
-  L.parts = L.end = L.dx;
+  L.parts = L.least = L.end = L.dx;
   if (shift == kDisBwdShift && distill_few(T, H, V)) {
     const size_t nc = static_cast<size_t>(ceil_div(V, vchunk(V)));
     L.parts = L.dx + align256(t * nc * vchunk(V) * 2);
@@ -1422,7 +1425,7 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
     return RLK_ERR_MISALIGNED;
   const Layout L = layout(T, H, V);
   const DistillLayout DL = distill_layout(L.bwd_end, T, H, V, K, kDisBwdShift);
-  if (workspace_bytes < DL.end) return RLK_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < DL.least) return RLK_ERR_WORKSPACE_TOO_SMALL;
   if ((s = check_device(&sms)) != RLK_OK) return s;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const DistillRows D = distill_rows(ws, DL, K);
@@ -1432,7 +1435,7 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
   if ((s = enqueue_distill_prep(teacher_ids, teacher_logits, logits_type, teacher_lse, T, V, K,
                                 teacher_temperature, kDisBwdShift, D, st)) != RLK_OK)
     return s;
-  const bool few = distill_few(T, H, V);
+  const bool few = distill_few(T, H, V) && workspace_bytes >= DL.end;
   float* parts = few ? reinterpret_cast<float*>(ws + DL.parts) : nullptr;
   if ((s = enqueue_bwd(hidden, W, nullptr, T, H, V, 0, V, temperature, lse, nullptr, nullptr, nullptr,
                        dHidden, parts, T, pl.NC, static_cast<float*>(dW), ws, L, st, kWaitLimitNs, 0,
