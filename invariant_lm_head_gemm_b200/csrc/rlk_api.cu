@@ -2,6 +2,7 @@
 // workspace layout, TMA tensor-map encoding and the launch sequences of the
 // forward and backward passes.  No allocation, no host synchronisation
 // (except rlk_read_device_error), no fallback path.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -1246,11 +1247,9 @@ rlk_status rlk_linear_logp_fwd_noalloc(const rlk_bf16* hidden, const rlk_bf16* W
 namespace rlk {
 namespace {
 
-// The sorted slots and their table behind a pass's own scratch, from `base`, up to
-// `least`: what the pass needs; in a backward of few rows the dX of all chunks and
-// their dHidden products, up to `end`: what its order for few rows takes.
+// The sorted slots and their table behind a pass's own scratch, from `base`.
 struct DistillLayout {
-  size_t ids, logq, y, sum, count, head, dx, parts, least, end;
+  size_t ids, logq, y, sum, count, head, end;
   int64_t G;
 };
 
@@ -1260,19 +1259,20 @@ struct DistillLayout {
 // to do: 161 us at T = 513, H = 1024, V = 32768 and 149 at T = 31, H = 576, V = 54485
 // (frozen head), against 121 and 75 here.  With ceil(T / 256) H above 8192 the pairs
 // are busy either way (T = 1024, H = 4096, V = 151936: 3232 and 3114; T = 4000, H = 512,
-// V = 65536: 745 and 783) and the other order needs less memory: here all of dX, at
-// most kFewBytes, and 4 T H bytes per chunk of 8192.  Both give the same bits, so a
-// workspace that has no room for that (one sized for more rows than this order is
-// for can be the smaller one) gets the other order.
+// V = 65536: 745 and 783) and the other order needs less memory: here all of dX and
+// 4 T H bytes per chunk of 8192, at most kFewBytes each.  Both give the same bits,
+// so a workspace that has no room for this one (sized for more rows than it is for,
+// it can be the smaller) gets the other.
 constexpr int64_t kFewTiles = 8192;
 constexpr int64_t kFewBytes = int64_t{256} << 20;
 
 bool distill_few(int64_t T, int64_t H, int64_t V) {
   const int64_t nc = ceil_div(V, vchunk(V));
-  return nc > 1 && ceil_div(T, kPairM) * H <= kFewTiles && T * nc * vchunk(V) * 2 <= kFewBytes;
+  return nc > 1 && ceil_div(T, kPairM) * H <= kFewTiles && T * nc * vchunk(V) * 2 <= kFewBytes &&
+         T * nc * H * 4 <= kFewBytes;
 }
 
-DistillLayout distill_layout(size_t base, int64_t T, int64_t H, int64_t V, int64_t K, int shift) {
+DistillLayout distill_layout(size_t base, int64_t T, int64_t V, int64_t K, int shift) {
   DistillLayout L;
   const size_t t = static_cast<size_t>(T), k = static_cast<size_t>(K);
   L.G = ceil_div(V, int64_t{1} << shift);
@@ -1282,14 +1282,27 @@ DistillLayout distill_layout(size_t base, int64_t T, int64_t H, int64_t V, int64
   L.sum = L.y + align256(t * k * 4);
   L.count = L.sum + align256(t * 4);
   L.head = L.count + align256(t * 4);
-  L.dx = L.head + align256(t * static_cast<size_t>(L.G) * sizeof(uint2));
-  L.parts = L.least = L.end = L.dx;
-  if (shift == kDisBwdShift && distill_few(T, H, V)) {
-    const size_t nc = static_cast<size_t>(ceil_div(V, vchunk(V)));
-    L.parts = L.dx + align256(t * nc * vchunk(V) * 2);
-    L.end = L.parts + align256(nc * t * H * 4);
-  }
+  L.end = L.head + align256(t * static_cast<size_t>(L.G) * sizeof(uint2));
   return L;
+}
+
+// The order for few rows: its counters, the slots, dX of all chunks and their dHidden
+// products; no chunk buffers and no accumulator.
+struct FewLayout {
+  size_t cnt, dx, parts, end;
+  DistillLayout rows;
+};
+
+FewLayout few_layout(int64_t T, int64_t H, int64_t V, int64_t K) {
+  FewLayout F;
+  const BwdPlan pl = bwd_plan(T, H, V);
+  const size_t t = static_cast<size_t>(T), nc = static_cast<size_t>(pl.NC);
+  F.cnt = kHeader;
+  F.rows = distill_layout(F.cnt + align256(bwd_counter_words(pl) * 4), T, V, K, kDisBwdShift);
+  F.dx = F.rows.end;
+  F.parts = F.dx + align256(t * nc * static_cast<size_t>(pl.ldx) * 2);
+  F.end = F.parts + align256(nc * t * static_cast<size_t>(H) * 4);
+  return F;
 }
 
 DistillRows distill_rows(uint8_t* ws, const DistillLayout& L, int64_t K) {
@@ -1343,9 +1356,10 @@ size_t rlk_linear_distill_workspace_bytes(int64_t T, int64_t H, int64_t V, int64
                                           int for_backward) {
   if (check_distill(T, H, V, K, 1.f, 1.f, RLK_TYPE_F32) != RLK_OK) return 0;
   const Layout L = layout(T, H, V);
-  const size_t fwd = distill_layout(L.fwd_end, T, H, V, K, kDisFwdShift).end;
-  const size_t bwd = distill_layout(L.bwd_end, T, H, V, K, kDisBwdShift).end;
-  return for_backward ? std::max(fwd, bwd) : fwd;
+  const size_t fwd = distill_layout(L.fwd_end, T, V, K, kDisFwdShift).end;
+  if (!for_backward) return fwd;
+  const size_t bwd = distill_layout(L.bwd_end, T, V, K, kDisBwdShift).end;
+  return std::max({fwd, bwd, distill_few(T, H, V) ? few_layout(T, H, V, K).end : 0});
 }
 
 rlk_status rlk_linear_distill_fwd(const rlk_bf16* hidden, const rlk_bf16* W,
@@ -1364,7 +1378,7 @@ rlk_status rlk_linear_distill_fwd(const rlk_bf16* hidden, const rlk_bf16* W,
       !aligned(teacher_lse, 4) || !aligned(loss, 4) || !aligned(lse, 4))
     return RLK_ERR_MISALIGNED;
   const Layout L = layout(T, H, V);
-  const DistillLayout DL = distill_layout(L.fwd_end, T, H, V, K, kDisFwdShift);
+  const DistillLayout DL = distill_layout(L.fwd_end, T, V, K, kDisFwdShift);
   if (workspace_bytes < DL.end) return RLK_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if ((s = check_device(&sms)) != RLK_OK) return s;
@@ -1423,9 +1437,19 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
       !aligned(teacher_logits, logits_type == RLK_TYPE_F32 ? 4 : 2) || !aligned(teacher_lse, 4) ||
       !aligned(lse, 4) || !aligned(dloss, 4))
     return RLK_ERR_MISALIGNED;
-  const Layout L = layout(T, H, V);
-  const DistillLayout DL = distill_layout(L.bwd_end, T, H, V, K, kDisBwdShift);
-  if (workspace_bytes < DL.least) return RLK_ERR_WORKSPACE_TOO_SMALL;
+  Layout L = layout(T, H, V);
+  DistillLayout DL = distill_layout(L.bwd_end, T, V, K, kDisBwdShift);
+  if (workspace_bytes < DL.end) return RLK_ERR_WORKSPACE_TOO_SMALL;
+  FewLayout F = {};
+  bool few = distill_few(T, H, V);
+  if (few) {
+    F = few_layout(T, H, V, K);
+    few = workspace_bytes >= F.end;
+  }
+  if (few) {
+    L.cnt = F.cnt;
+    DL = F.rows;
+  }
   if ((s = check_device(&sms)) != RLK_OK) return s;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const DistillRows D = distill_rows(ws, DL, K);
@@ -1435,12 +1459,11 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
   if ((s = enqueue_distill_prep(teacher_ids, teacher_logits, logits_type, teacher_lse, T, V, K,
                                 teacher_temperature, kDisBwdShift, D, st)) != RLK_OK)
     return s;
-  const bool few = distill_few(T, H, V) && workspace_bytes >= DL.end;
-  float* parts = few ? reinterpret_cast<float*>(ws + DL.parts) : nullptr;
+  float* parts = few ? reinterpret_cast<float*>(ws + F.parts) : nullptr;
   if ((s = enqueue_bwd(hidden, W, nullptr, T, H, V, 0, V, temperature, lse, nullptr, nullptr, nullptr,
                        dHidden, parts, T, pl.NC, static_cast<float*>(dW), ws, L, st, kWaitLimitNs, 0,
                        nullptr, 0, &D, dloss, dW_type == RLK_TYPE_BF16,
-                       few ? ws + DL.dx : nullptr)) != RLK_OK)
+                       few ? ws + F.dx : nullptr)) != RLK_OK)
     return s;
   return few ? rlk_dhidden_combine(parts, pl.NC, T * H, dHidden, stream) : RLK_OK;
 }

@@ -54,3 +54,15 @@ def test_the_least_workspace_of_the_backward(L, T, H, V, K):
     assert _bwd(L, T=T, H=H, V=V, K=K, wsb=least) == DEVICE
     assert _bwd(L, T=T, H=H, V=V, K=K, wsb=least - 1) == WS_SMALL
     assert L.rlk_linear_distill_workspace_bytes(T, H, V, K, 1) >= least
+
+
+def test_the_few_row_order_keeps_to_its_bounds(L):
+    """All of dX and one dHidden product per chunk, at most 256 MB each, beside the
+    teacher's rows: not the chunk buffers that the order does not use."""
+    f = L.rlk_linear_distill_workspace_bytes
+    T, H, V, K = 512, 4096, 151936, 64
+    rows = 3 * _a(T * K * 4) + 2 * _a(T * 4) + _a(T * 594 * 8)
+    nc = 19
+    assert f(T, H, V, K, 1) <= T * nc * 8192 * 2 + T * nc * H * 4 + rows + (1 << 16)
+    T, H, V, K = 256, 8192, 524288, 8              # the products alone would take 512 MB
+    assert f(T, H, V, K, 1) == max(_least(T, H, V, K), f(T, H, V, K, 0))
