@@ -745,15 +745,23 @@ def _dis():
     return _dis_fns
 
 
-def make_distill_workspace(T: int, H: int, V: int, K: int, for_backward: bool = True, device=None):
-    """A workspace tensor (uint8) for the distillation of up to T rows with up to K
-    slots, its error word zeroed."""
+def _distill_bytes(T, H, V, K, for_backward):
     n = int(_dis().rlk_linear_distill_workspace_bytes(T, H, V, K, 1 if for_backward else 0))
     if n == 0:
         raise ValueError("unsupported sizes T=%d H=%d V=%d K=%d" % (T, H, V, K))
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return n
+
+
+def _distill_space(n, device):
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws
+
+
+def make_distill_workspace(T: int, H: int, V: int, K: int, for_backward: bool = True, device=None):
+    """A workspace tensor (uint8) for the distillation of up to T rows with up to K
+    slots, its error word zeroed."""
+    return _distill_space(_distill_bytes(T, H, V, K, for_backward), device or "cuda")
 
 
 def _distill_args(hidden, W, teacher_ids, teacher_logits, teacher_lse):
@@ -841,22 +849,33 @@ def _distill_bwd(sizes, hidden, W, ids, logits, temperature, teacher_temperature
     return dHidden, dW
 
 
+# A workspace up to this size is kept from the forward for the backward: allocating
+# and clearing another takes 20 us of host time, which a small step feels (135 us
+# against 156 at T = 64, H = 256, V = 1024).  Larger ones (hundreds of MB) would add to
+# the activations that are held at the forward's end.
+_HELD_BYTES = 1 << 20
+
+
 class LinearDistill(torch.autograd.Function):
     """autograd wrapper: loss [T] = LinearDistill.apply(hidden, W, teacher_ids,
     teacher_logits, temperature, teacher_temperature=None, teacher_lse=None).
-    Gradients flow to hidden and W (bf16); a W that needs none costs none."""
+    Gradients flow to hidden and W (bf16); a W that needs none costs none.  Between
+    the passes the inputs, lse and at most 1 MB of workspace are held: where a
+    backward takes more, it allocates it for itself."""
 
     @staticmethod
     def forward(ctx, hidden, W, teacher_ids, teacher_logits, temperature=1.0,
                 teacher_temperature=None, teacher_lse=None):
-        T, H = hidden.shape
-        ws = make_distill_workspace(T, H, W.shape[0], teacher_ids.shape[1],
-                                    any(ctx.needs_input_grad[:2]), hidden.device)
+        ctx.ws = None
+        if any(ctx.needs_input_grad[:2]):
+            T, H = hidden.shape
+            n = _distill_bytes(T, H, W.shape[0], teacher_ids.shape[1], True)
+            if n <= _HELD_BYTES:
+                ctx.ws = _distill_space(n, hidden.device)
         loss, lse = rlk_linear_distill_fwd(hidden, W, teacher_ids, teacher_logits, temperature,
-                                           teacher_temperature, teacher_lse, ws)
+                                           teacher_temperature, teacher_lse, ctx.ws)
         ctx.save_for_backward(hidden, W, teacher_ids, teacher_logits, teacher_lse, lse)
         ctx.temperatures = (temperature, teacher_temperature)
-        ctx.ws = ws
         return loss
 
     @staticmethod
