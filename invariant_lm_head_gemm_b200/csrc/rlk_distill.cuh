@@ -199,9 +199,11 @@ struct EpiDistill {
     st.valid = row < p.T;
     st.A = st.coef = st.all = 0.f;
     if (st.valid) {
+      const float Q = p.D.sum[row];
       st.A = p.lse[row] * kLog2e;
-      st.coef = p.inv_tau * p.dloss[row];
-      st.all = st.coef * p.D.sum[row];
+      // a row without weight has no gradient, not even 0 times a NaN or an infinity
+      st.coef = Q == 0.f ? 0.f : p.inv_tau * p.dloss[row];
+      st.all = st.coef * Q;
     }
   }
 
