@@ -9,7 +9,6 @@
 // where the row sits, or on its alignment (an odd V puts every row at another
 // offset within 16 bytes).
 #include <algorithm>
-#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -812,8 +811,6 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) verify_kernel
   }
 }
 
-constexpr int kMaxSampDevices = 64;
-
 bool al(const void* p, uintptr_t m) { return reinterpret_cast<uintptr_t>(p) % m == 0; }
 
 template <typename Args>
@@ -840,23 +837,18 @@ rlk_status launch_clusters(void (*kern)(Args), const Args& a, int64_t groups, in
 
 template <typename TIn, typename TOut, int kThreads>
 rlk_status launch_probs_as(const ProbArgs& a, int C, cudaStream_t st) {
-  static std::atomic<bool> raised[kMaxSampDevices];  // the kernel's shared-memory limit
-  int dev = 0;
   auto kern = probs_kernel<TIn, TOut, kThreads>;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxSampDevices) {
+  const size_t smem = static_cast<size_t>(a.slice) * sizeof(TIn) + kProbPad;
+  // The limit is raised by every call that needs it (past 48 KB, less what the kernel
+  // holds statically), not once: it is a fact of the context, and goes with it when the
+  // device is reset.
+  if (smem > 40u * 1024u &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kProbSlice + kProbPad)) != cudaSuccess) {
     cudaGetLastError();
     return RLK_ERR_CUDA;
   }
-  if (!raised[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kProbSlice + kProbPad)) != cudaSuccess) {
-      cudaGetLastError();
-      return RLK_ERR_CUDA;
-    }
-    raised[dev].store(true, std::memory_order_release);
-  }
-  return launch_clusters(kern, a, a.R, C, kThreads, st,
-                         static_cast<size_t>(a.slice) * sizeof(TIn) + kProbPad);
+  return launch_clusters(kern, a, a.R, C, kThreads, st, smem);
 }
 
 template <typename TIn, typename TOut>
