@@ -348,7 +348,8 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
  * zeros; one with a NaN, with +inf at tau > 0, or with a row temperature that
  * is negative, not finite or so small that log2(e) / tau is not, as NaN; both
  * set RLK_DEVERR_PROBS.  probs may be the logits' own memory where type and
- * stride are equal.
+ * stride are equal (where they are not, RLK_ERR_INVALID_ARG); otherwise they must
+ * not overlap.
  * Sizes: 1 <= V < 2^31, R < 2^28, strides < 2^31.  R = 0 is a no-op.  One
  * launch.
  *

@@ -891,6 +891,9 @@ extern "C" rlk_status rlk_token_probs(const void* logits, int logits_type, int64
   if (!al(logits, logits_type == RLK_TYPE_F32 ? 4 : 2) || !al(probs, probs_type == RLK_TYPE_F32 ? 4 : 2) ||
       !al(row_temperature, 4) || !al(workspace, 256))
     return RLK_ERR_MISALIGNED;
+  // in place, a row's CTAs write where others still read unless type and stride are equal
+  if (probs == logits && (probs_type != logits_type || (R > 1 && ld_probs != ld_logits)))
+    return RLK_ERR_INVALID_ARG;
   if (workspace_bytes < kSampHeader) return RLK_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   rlk_status s = current_device_supported(&sms);
