@@ -369,8 +369,9 @@ rlk_status rlk_linear_distill_bwd(const rlk_bf16* hidden, const rlk_bf16* W,
  * and num_accepted [B] int64.  A draft outside [0, V) within its sequence's
  * length is not accepted and sets RLK_DEVERR_TARGET; where r has no positive
  * entry, or the row of p or of q that it is formed from holds a NaN or an
- * infinity, the drawn token is -1 and RLK_DEVERR_PROBS is set.  Strides may be 0 (shared rows).  K = 0 draws one token per sequence
- * (draft_tokens, u_accept, draft_probs are not read).
+ * infinity, the drawn token is -1 and RLK_DEVERR_PROBS is set.  Strides may be 0
+ * (shared rows).  K = 0 draws one token per sequence (draft_tokens, u_accept,
+ * draft_probs are not read).  The outputs must not overlap the inputs.
  * Sizes: 1 <= V < 2^31, K < 2^20, B < 2^28.  B = 0 is a no-op.  One launch. */
 size_t rlk_sampling_workspace_bytes(void);
 rlk_status rlk_token_probs(const void* logits, int logits_type, int64_t R, int64_t V,
