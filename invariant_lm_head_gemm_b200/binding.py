@@ -619,7 +619,8 @@ def _samp():
 
 def sampling_workspace(device=None):
     """The zeroed workspace (an error word) of rlk_token_probs and
-    rlk_draft_verify; calls may share it."""
+    rlk_draft_verify; calls may share it.  A call without one allocates and clears
+    its own, and what it would report there is lost."""
     return torch.zeros(int(_samp().rlk_sampling_workspace_bytes()), dtype=torch.uint8,
                        device=device or "cuda")
 
@@ -859,8 +860,9 @@ _HELD_BYTES = 1 << 20
 class LinearDistill(torch.autograd.Function):
     """autograd wrapper: loss [T] = LinearDistill.apply(hidden, W, teacher_ids,
     teacher_logits, temperature, teacher_temperature=None, teacher_lse=None).
-    Gradients flow to hidden and W (bf16); a W that needs none costs none.  Between
-    the passes the inputs, lse and at most 1 MB of workspace are held: where a
+    Gradients flow to hidden and W (bf16); a W that needs none costs none (a
+    hidden that needs none does: its product is part of the backward).  Between the
+    passes the inputs, lse and at most 1 MB of workspace are held: where a
     backward takes more, it allocates it for itself."""
 
     @staticmethod

@@ -397,7 +397,8 @@ rlk_status enqueue_fwd_partials_short(const rlk_bf16* hidden, const rlk_bf16* W,
 // same bits).  The short-batch kernel streams W without padding T to 256 rows, but
 // hands each row's triple from warp to warp and CTA to CTA, 16 chunks to a split;
 // where W is small that chain, not W, is its time.  Estimates in us of both, from
-// rounds over their units (74 pairs, 33 clusters):
+// rounds over their units (74 pairs, 33 clusters: the B200's 148 SMs, which is what
+// the library runs on; a part with fewer would get the same bits, at times later):
 //   pair:  8 + rounds max(6.5, 0.0128 H), a third more below 16 rows
 //   short: 16 + rounds (3 + 0.0043 H) + T (0.012 + 0.033 rounds)
 // and the pair kernel only where it is a tenth ahead.  Measured, short / pair, at

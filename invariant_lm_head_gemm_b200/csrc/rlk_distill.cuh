@@ -19,8 +19,11 @@
 // bound as the linear-logp kernels are.  Scoring 16 rows: 198 us, W's 1.25 GB at 0.96
 // of the measured copy rate.
 //
-// dX is rounded to bf16 for the two products, as in the linear-logp backward, so
-// gradients are off by about 1.7e-3 of their norm before their own rounding.
+// dX is rounded to bf16 for the two products, as in the linear-logp backward: the
+// tensor cores' 16-bit operands.  Gradients are off by about 1.7e-3 of their norm
+// before their own rounding, 2.4e-3 after it (an fp32 product rounded once: 1.7e-3);
+// carrying dX in two bf16 terms would add both products once more, half of the
+// backward's time.
 #pragma once
 
 #include <cstdint>

@@ -62,14 +62,24 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_
 // slice's alignment, so its order is the same for every row; the other two looks
 // take whole aligned vectors.
 //
-// Bound by HBM where there are many rows: each entry is read once and written
-// once, one CTA's copies running beside another's looks.  320 x 151936 fp32: 74.5 us,
-// 5.2 TB/s, 0.80 of the measured copy; 1027 x 50257 bf16 (half the bytes per entry, as
-// many instructions): 45 us, 0.70; one row of 151936: 6.6 us.  Few instructions per
-// entry is what that takes: holding the entries in registers instead (one look, one
-// exponential, but 64 warps to a row of 50257, each with its reductions) ran 55
-// instructions per entry and 128 us at 1027 x 50257.  Persistent CTAs were slower
-// (90 us at 320 x 151936), and so were 512 and 128 threads (91, 84).
+// Each entry is read once and written once, one CTA's copies running beside another's
+// looks.  320 x 151936 fp32: 74 us, 0.80 of the measured copy, bound by HBM; bf16 to
+// fp32 55 us, 0.81.  With fewer bytes per entry the looks weigh more, and neither HBM
+// nor issue is full: 1027 x 50257 bf16 45 us, HBM 0.70, issue slots 0.42; two CTAs per
+// SM, and each waits for all of its copies before its first look, so one CTA's looks are
+// all that covers the other's copies.  Where the types differ the stores are single
+// entries: fp32 to bf16 67 us at 320 x 151936, 0.66.  One row of 151936: 6.6 us.
+// Holding the entries in registers (one look, one exponential, but 64 warps to a row of
+// 50257, each with its reductions) ran 55 instructions per entry and 128 us at
+// 1027 x 50257.  Persistent CTAs with the same three looks took 94 us at 320 x 151936
+// and 54 at 1027 x 50257; 512 threads 91 and 46, 128 threads 84 and 54.
+//
+// Precision, of fp32 results: the factor k, each exponent, ex2.approx (2 units in
+// the last place), 1 / S and the product are rounded to fp32, so an entry D powers of two
+// below the maximum is off by up to (3 D + 10) 2^-24 relative; in the norm 1.1e-7 from
+// fp64 at the measured cases, where expf and a division give 6e-8.  Splitting k or a
+// longer exponential would cost an instruction or more per entry and look; the
+// verification that follows compares with random numbers of 24 bits.
 constexpr int kProbMaxCluster = 8;
 constexpr int kProbThreads = 256;
 constexpr uint32_t kProbSlice = 100u * 1024u;  // bytes of a slice at most
@@ -394,8 +404,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 4) probs_kerne
   }
 }
 
-// Rows that no cluster's shared memory holds: one CTA per row and eighth, its
-// entries read again from L2 or HBM for the second and third look.
+// Rows that no cluster's shared memory holds (more than 204800 entries in fp32, 409600
+// in bf16): one CTA per row and eighth, its entries read again from L2 or HBM for the
+// second and third look, one at a time.  262144 fp32: one row 17 us, 320 rows 206 us (0.50
+// of the measured copy, where 320 rows of 204800 take 108, 0.74); 409601 bf16: 28 and
+// 287 us (0.28).
 constexpr int kProbLongThreads = 512;
 constexpr int kProbLongWarps = kProbLongThreads / 32;
 
@@ -479,9 +492,12 @@ __global__ void __launch_bounds__(kProbLongThreads) probs_long_kernel(const Prob
 //
 // Bound by latency at few sequences (the drafts, their entries, the row, the
 // walk: four round trips and a cluster barrier): one of 4 drafts and V = 151936 7.6 us.
-// At many, by HBM once those are over: 64 sequences 19.5 us, 78 MB of rows in 11 of
-// them; in bf16 (half the bytes per load) by the loads under way: 256 rows of 151936
-// 50 us, 3.1 TB/s.  What did not help: copies through shared memory ahead of the sums
+// At many in fp32, by HBM once those are over: 64 sequences 19.5 us, 78 MB of rows in 11
+// of them.  In bf16 by instructions and latency together: 256 ragged sequences of V =
+// 50257 24.6 us against 7.9 of bytes; 10.8 M warp instructions, 27 per 32 entries
+// of a row (p and q), come to 11 us of issue on the SMs that hold two of the 256 CTAs (issuing in
+// 63% of their active cycles), the rest is loads waited for and the fixed trips; 256
+// rows of 151936 50 us, 3.1 TB/s, 24.8 M instructions, 68%.  What did not help: copies through shared memory ahead of the sums
 // (26 us at 64), several segments' loads at once or the next one's ahead in registers
 // (21), 256 threads (19.1, but 9.3 at one).
 constexpr int kVerThreads = 512;
