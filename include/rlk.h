@@ -295,8 +295,9 @@ rlk_status rlk_transition_logp(const float* x, const float* v, const float* prev
  *    (its logit is not looked at).  Ids may come in any order; an id given twice
  *    counts twice.  teacher_logits [T][K] of logits_type; -inf weighs nothing.
  *    A row without a used slot, or with all of them at -inf, has loss 0 and no
- *    gradient, whatever its dloss.  Any other id outside [0, V) sets RLK_DEVERR_TARGET (forward) and
- *    makes the row's loss NaN; both passes leave the slot out.
+ *    gradient, whatever its dloss.  Any other id outside [0, V) sets
+ *    RLK_DEVERR_TARGET (forward) and makes the row's loss NaN; both passes leave
+ *    the slot out.
  *  - teacher_lse [T] fp32 or NULL.  1 <= K <= 256 (more:
  *    RLK_ERR_UNSUPPORTED_SHAPE); teacher_temperature > 0 and finite.
  *  - fwd writes loss [T] and lse [T] fp32; lse equals rlk_linear_logp_fwd's bit

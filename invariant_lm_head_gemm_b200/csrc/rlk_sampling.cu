@@ -74,8 +74,8 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_
 // 1027 x 50257.  Persistent CTAs with the same three looks took 94 us at 320 x 151936
 // and 54 at 1027 x 50257; 512 threads 91 and 46, 128 threads 84 and 54.
 //
-// Precision, of fp32 results: the factor k, each exponent, ex2.approx (2 units in
-// the last place), 1 / S and the product are rounded to fp32, so an entry D powers of two
+// Precision, of fp32 results: the factor k, each exponent, ex2.approx (2^-22),
+// 1 / S and the product are rounded to fp32, so an entry D powers of two
 // below the maximum is off by up to (3 D + 10) 2^-24 relative; in the norm 1.1e-7 from
 // fp64 at the measured cases, where expf and a division give 6e-8.  Splitting k or a
 // longer exponential would cost an instruction or more per entry and look; the
@@ -494,12 +494,13 @@ __global__ void __launch_bounds__(kProbLongThreads) probs_long_kernel(const Prob
 // walk: four round trips and a cluster barrier): one of 4 drafts and V = 151936 7.6 us.
 // At many in fp32, by HBM once those are over: 64 sequences 19.5 us, 78 MB of rows in 11
 // of them.  In bf16 by instructions and latency together: 256 ragged sequences of V =
-// 50257 24.6 us against 7.9 of bytes; 10.8 M warp instructions, 27 per 32 entries
-// of a row (p and q), come to 11 us of issue on the SMs that hold two of the 256 CTAs (issuing in
-// 63% of their active cycles), the rest is loads waited for and the fixed trips; 256
-// rows of 151936 50 us, 3.1 TB/s, 24.8 M instructions, 68%.  What did not help: copies through shared memory ahead of the sums
-// (26 us at 64), several segments' loads at once or the next one's ahead in registers
-// (21), 256 threads (19.1, but 9.3 at one).
+// 50257 24.6 us against 7.9 of bytes; 10.8 M warp instructions, 27 per 32 entries of a
+// row (p and q), come to 11 us of issue on the SMs that hold two of the 256 CTAs
+// (issuing in 63% of their active cycles), the rest is loads waited for and the fixed
+// trips; 256 rows of 151936 50 us, 3.1 TB/s, 24.8 M instructions, 68%.  What did not
+// help: copies through shared memory ahead of the sums (26 us at 64), several segments'
+// loads at once or the next one's ahead in registers (21), 256 threads (19.1, but 9.3 at
+// one).
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerMaxCluster = 8;
